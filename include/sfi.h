@@ -346,6 +346,150 @@ sfi_status sfi_get_wait_limit(int64_t* ns);
 sfi_status sfi_selftest_wait(const sfi_paged_kv* kv, int64_t limit_ns, sfi_stream stream);
 
 /* ------------------------------------------------------------------------
+ * 8-bit paged cache.  The pages name no 8-bit cache: this is an addition of
+ * the library, for callers whose contexts outgrow a bf16 cache.
+ *
+ * Full pages (16 tokens of one KV head) hold 8-bit codes with one fp32 scale
+ * for the page's keys and one for its values: value = code * scale.  The
+ * tokens of a page that is not full yet are kept in bf16 (the tail), so every
+ * value is rounded exactly once, when its page fills:
+ *   amax  = max |x| over the page's 16 x D values, at least 2^-100
+ *   scale = amax / Q,  code = round(x * (Q / amax)), ties to even,
+ *   Q = 448 (SFI_FMT_E4M3) or 127 (SFI_FMT_INT8), all in fp32.
+ * A page holding an infinity or a NaN stores a NaN scale (and codes 0): all of
+ * it stands for NaN.  The NaN codes of e4m3 are never written and must not be
+ * handed in.
+ *
+ * Lengths.  Every call below takes L and lens: with lens == NULL each sequence
+ * has L tokens; else lens (device int32 [B]) gives each sequence's own, in
+ * [0, L] (0: an empty sequence).  L sizes the launch, so a captured call can be
+ * replayed while the lengths in lens grow up to L.  An entry outside [0, L]
+ * is latched as SFI_ERR_DEVICE_CHECK and its sequence treated as empty. */
+typedef enum { SFI_FMT_E4M3 = 0, SFI_FMT_INT8 = 1 } sfi_quant_format;
+
+/*  k_pool, v_pool    uint8 [num_pages, Hkv, 16, D]: codes, 16-byte aligned
+ *  k_scale, v_scale  fp32  [num_pages, Hkv]
+ *  k_tail, v_tail    bf16  [B, Hkv, 16, D], 16-byte aligned: row r is token
+ *                    16 * (len / 16) + r of the sequence while r < len % 16
+ *  page_table        int32 [B, max_pages]
+ *  err               int32 device word for latched errors, or NULL
+ *  format            sfi_quant_format */
+typedef struct {
+  uint8_t* k_pool;
+  uint8_t* v_pool;
+  float* k_scale;
+  float* v_scale;
+  sfi_bf16* k_tail;
+  sfi_bf16* v_tail;
+  const int32_t* page_table;
+  int32_t* err;
+  int32_t format;
+} sfi_quant_kv;
+
+/* Block index: bounds of the keys of every full page, for sfi_block_select.
+ *  bounds      int8 [num_pages, Hkv, 2, D], 16-byte aligned: per dimension the
+ *              largest (0) and smallest (1) key value of the page, divided by
+ *              the page's scale and rounded up (0) and down (1)
+ *  scale       fp32 [num_pages, Hkv]: the smallest power of two u >= 2^-126
+ *              with max |k| <= 127 u
+ *  page_table  int32 [B, max_pages], the cache's
+ *  err         int32 device word for latched errors, or NULL
+ * In a page's bounds a NaN counts as 0 and an infinity as the largest finite
+ * bf16 value. */
+typedef struct {
+  int8_t* bounds;
+  float* scale;
+  const int32_t* page_table;
+  int32_t* err;
+} sfi_block_index;
+
+/* Takes the tokens [pos_lo, len) of a bf16 paged cache into the 8-bit cache
+ * (after a prefill, or chunk by chunk): full pages as codes, the remaining
+ * rows into the tail; rows of the tail at or past len % 16 are left as they
+ * were.  pos_lo: a multiple of 16; L may be 0.  index (may be NULL) receives
+ * the bounds of the same full pages.  kv and qkv each go by their own page
+ * table (shape gives max_pages and num_pages of both). */
+sfi_status sfi_quant_store(const sfi_shape* shape, const sfi_paged_kv* kv, const sfi_quant_kv* qkv,
+                           const sfi_block_index* index, int32_t pos_lo, int32_t L, const int32_t* lens,
+                           sfi_stream stream);
+
+/* Appends one token per (sequence, KV head) at position len - 1 (L and lens
+ * count it; an empty sequence gets none): its tail row, and, when it fills its
+ * page, the page's codes and scales from the 16 tail rows and (index non-NULL)
+ * its bounds.  k_new, v_new: bf16 [B, Hkv, D], 16-byte aligned. */
+sfi_status sfi_quant_append(const sfi_shape* shape, const sfi_quant_kv* qkv, const sfi_block_index* index,
+                            int32_t L, const int32_t* lens, const sfi_bf16* k_new, const sfi_bf16* v_new,
+                            sfi_stream stream);
+
+/* Writes the tokens [pos_lo, len) of the 8-bit cache into a bf16 paged cache
+ * (code * scale rounded to bf16; the tail's rows as they are), e.g. for
+ * sfi_compact.  pos_lo: a multiple of 16.  Rows at or past len are left as
+ * they were; key norms are not touched. */
+sfi_status sfi_quant_load(const sfi_shape* shape, const sfi_quant_kv* qkv, const sfi_paged_kv* kv,
+                          int32_t pos_lo, int32_t L, const int32_t* lens, sfi_stream stream);
+
+/* Decode attention over [0, len) of the 8-bit cache.
+ *  q    bf16 [B, Hq, D], 16-byte aligned
+ *  out  fp32 [B, Hq, D] = sum_j softmax(z)_j v_j, z_j = q.k_j / sqrt(D)
+ *  lse  fp32 [B, Hq] natural-log sum of exp(z), or NULL
+ * An empty sequence gets out = 0 and lse = -infinity.  ws: scratch of
+ * sfi_block_workspace_size bytes, 16-byte aligned; it needs no clearing.
+ * Calls that share one ws must not run concurrently. */
+sfi_status sfi_quant_attn(const sfi_shape* shape, const sfi_quant_kv* qkv, int32_t L, const int32_t* lens,
+                          const sfi_bf16* q, float* out, float* lse, void* ws, size_t ws_bytes,
+                          sfi_stream stream);
+
+/* Reads and clears the latched error word of an 8-bit cache (synchronous). */
+sfi_status sfi_quant_poll_error(const sfi_quant_kv* qkv, int32_t* code);
+
+/* ------------------------------------------------------------------------
+ * Block-sparse decode attention: every (sequence, KV head) attends to K of its
+ * pages ("blocks" of 16 tokens), picked by a bound on their attention logits.
+ * An addition of the library beside the pages' slow/fast steps: it needs no
+ * dense step to refresh a selection. */
+
+/* Bounds of the full pages among the tokens [pos_lo, len) of a bf16 paged
+ * cache into index.  pos_lo: a multiple of 16; L may be 0.  After
+ * sfi_append_kv, call it with pos_lo = L - 16 when L % 16 == 0. */
+sfi_status sfi_block_build(const sfi_shape* shape, const sfi_paged_kv* kv, const sfi_block_index* index,
+                           int32_t pos_lo, int32_t L, const int32_t* lens, sfi_stream stream);
+
+/* Bytes of scratch for sfi_block_select, sfi_block_attn, sfi_quant_attn and
+ * sfi_quant_block_attn at contexts up to max_pages * 16 tokens. */
+sfi_status sfi_block_workspace_size(const sfi_shape* shape, size_t* bytes);
+
+/* The K blocks of every (sequence, KV head) with the largest scores, ascending,
+ * into sel int32 [B, Hkv, sel_ld].  The score of block j is
+ *   u_j = max over the group's heads h of  e_h * scale_j *
+ *         sum_d max(q^_hd * hi_jd, q^_hd * lo_jd)
+ * with q^ = round(q / e_h), e_h the smallest power of two >= 2^-126 with
+ * max |q_h| <= 127 e_h (NaN counts as 0, an infinity as the largest finite
+ * value): integers times powers of two, so u is exact in fp32 (clamped to the
+ * finite range) and the selection a function of the inputs alone.  Ties go to
+ * the lower block.  Blocks that hold one of the first n_sink or the last
+ * n_recent tokens are always taken; only the bounds of other blocks, which are
+ * full, are read.  K must be at most ceil(L / 16) and at least the smaller of
+ * that and ceil(n_sink / 16) + ceil(n_recent / 16) + 1, n_recent >= 1
+ * (SFI_ERR_SHAPE); ceil(L / 16) <= 262144 and B * Hkv <= 65535
+ * (SFI_ERR_UNSUPPORTED).  A sequence of at most K blocks gets 0 .. K - 1: the
+ * attention below passes over blocks at or past its end.  q as above. */
+sfi_status sfi_block_select(const sfi_shape* shape, const sfi_block_index* index, int32_t L, const int32_t* lens,
+                            const sfi_bf16* q, int32_t n_sink, int32_t n_recent, int32_t K, int32_t* sel,
+                            int32_t sel_ld, void* ws, size_t ws_bytes, sfi_stream stream);
+
+/* Decode attention over the listed blocks of a bf16 paged cache and of an 8-bit
+ * cache: the tokens below len of blocks sel[b, g, 0 .. K).  Entries outside
+ * [0, ceil(len / 16)) are passed over; a block listed twice counts twice.  No
+ * token left: out = 0, lse = -infinity.  The other arguments are those of
+ * sfi_quant_attn.  sel_ld >= K >= 1. */
+sfi_status sfi_block_attn(const sfi_shape* shape, const sfi_paged_kv* kv, int32_t L, const int32_t* lens,
+                          const sfi_bf16* q, const int32_t* sel, int32_t sel_ld, int32_t K, float* out,
+                          float* lse, void* ws, size_t ws_bytes, sfi_stream stream);
+sfi_status sfi_quant_block_attn(const sfi_shape* shape, const sfi_quant_kv* qkv, int32_t L, const int32_t* lens,
+                                const sfi_bf16* q, const int32_t* sel, int32_t sel_ld, int32_t K, float* out,
+                                float* lse, void* ws, size_t ws_bytes, sfi_stream stream);
+
+/* ------------------------------------------------------------------------
  * Decode-step driver ([ES] §2 trigger, §3 item 1 asynchronous pipeline;
  * [ZH] §2.3 双 CUDA 流).  A context owns one side stream and per-layer events;
  * the caller owns every tensor and the context workspace.

@@ -82,10 +82,6 @@ WsLayout ws_layout(const sfi_shape& s, const sfi_params& p) {
   return w;
 }
 
-namespace {
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 sfi_status check_shape(const sfi_shape* s) {
   if (!s) return SFI_ERR_INVALID_ARG;
   if (s->B < 1 || s->Hq < 1 || s->Hkv < 1 || s->Hq % s->Hkv != 0) return SFI_ERR_SHAPE;
@@ -100,6 +96,19 @@ sfi_status check_shape(const sfi_shape* s) {
   return SFI_OK;
 }
 
+sfi_status check_kv(const sfi_paged_kv* kv) {
+  if (!kv || !kv->k_pool || !kv->v_pool || !kv->page_table) return SFI_ERR_INVALID_ARG;
+  if (!aligned16(kv->k_pool) || !aligned16(kv->v_pool)) return SFI_ERR_INVALID_ARG;
+  return SFI_OK;
+}
+
+sfi_status check_L(const sfi_shape* s, int L) {
+  if (L < 1 || L > s->max_pages * kPage) return SFI_ERR_SHAPE;
+  return SFI_OK;
+}
+
+namespace {
+
 sfi_status check_params(const sfi_params* p) {
   if (!p) return SFI_ERR_INVALID_ARG;
   if (p->n_sink < 0 || p->n_recent < 1 || p->k_fixed < 0 || p->nms_window < 0) return SFI_ERR_INVALID_ARG;
@@ -110,17 +119,6 @@ sfi_status check_params(const sfi_params* p) {
   if (p->refresh_budget < 1) return SFI_ERR_INVALID_ARG;
   if (p->evidence_window < 0 || p->evidence_window > 32 || p->evidence_window > p->n_recent)
     return SFI_ERR_INVALID_ARG;
-  return SFI_OK;
-}
-
-sfi_status check_kv(const sfi_paged_kv* kv) {
-  if (!kv || !kv->k_pool || !kv->v_pool || !kv->page_table) return SFI_ERR_INVALID_ARG;
-  if (!aligned16(kv->k_pool) || !aligned16(kv->v_pool)) return SFI_ERR_INVALID_ARG;
-  return SFI_OK;
-}
-
-sfi_status check_L(const sfi_shape* s, int L) {
-  if (L < 1 || L > s->max_pages * kPage) return SFI_ERR_SHAPE;
   return SFI_OK;
 }
 

@@ -47,6 +47,7 @@ enum ErrSite : int {
   kSiteAppend = 1, kSiteNorms = 2, kSiteAttnProducer = 3, kSiteAttnConsumer = 4,
   kSiteAttnPage = 5, kSiteAttnRows = 6, kSiteCompactIdx = 7, kSiteCompactPage = 8,
   kSiteSelectPage = 9, kSiteCompactRows = 10, kSiteSelfTest = 11,
+  kSiteLens = 12, kSiteQuantPage = 13, kSiteBlockPage = 14, kSitePageAttn = 15,
 };
 
 __device__ __forceinline__ void latch_error(int* err, int status, int site) {
@@ -234,6 +235,25 @@ __device__ __forceinline__ void named_barrier(int id, int nthreads) {
 __device__ __forceinline__ uint32_t float_key(float f) {
   uint32_t u = __float_as_uint(f);
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
+// The smallest e >= -126 with amax <= 127 * 2^e (amax finite, >= 0): the
+// exponent field gives 2^x <= amax < 2^(x+1), and amax / 2^x is at most
+// 127 / 64 = 1.984375 unless its mantissa field exceeds 0x7e0000.
+__device__ __forceinline__ int unit_exponent(float amax) {
+  const uint32_t u = __float_as_uint(amax);
+  const int e = (int)(u >> 23) - 133 + ((u & 0x7fffffu) > 0x7e0000u ? 1 : 0);
+  return max(e, -126);
+}
+
+// Length of sequence b: L, or lens[b].  An entry outside [0, L] is latched and
+// the sequence treated as empty.
+__device__ __forceinline__ int seq_len(const int32_t* lens, int L, int b, int* err) {
+  if (!lens) return L;
+  const int n = lens[b];
+  if ((unsigned)n <= (unsigned)L) return n;
+  latch_error(err, SFI_ERR_DEVICE_CHECK, kSiteLens);
+  return 0;
 }
 
 // Append of one decode token by one warp: row `pos` of (b, kv head h) in the

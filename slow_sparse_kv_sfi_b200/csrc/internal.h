@@ -117,6 +117,13 @@ struct StepToken {
   const sfi_bf16* v_new;
 };
 
+// Argument checks shared by the entry points (api.cu): sizes of a layer, a
+// bf16 paged cache, a context length, and pointers copied 16 bytes at a time.
+sfi_status check_shape(const sfi_shape* s);
+sfi_status check_kv(const sfi_paged_kv* kv);
+sfi_status check_L(const sfi_shape* s, int L);
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
 // Validation of a dense-attention call's shape, cache, length, query, output
 // and extras (api.cu); SFI_OK or the status the entry points return.
 sfi_status check_dense_call(const sfi_shape* shape, const sfi_paged_kv* kv, int32_t L, const sfi_bf16* q,
@@ -190,5 +197,18 @@ sfi_status run_idx_to_bits(const sfi_shape& s, const sfi_params& p, const sfi_pa
 int compact_tiles(int nC);
 int score_tile(int G);
 int stat_chunks(int nC);
+
+
+// Block-sparse and 8-bit calls: scratch is [scores][partials (O)][partials (m, l)].
+struct BlockWs {
+  size_t score_off, part_off, ml_off, total;
+};
+BlockWs block_ws(const sfi_shape& s);
+// Chunks per (sequence, KV head) that sfi_block_attn and its kin cut T tiles
+// into, and its largest value over contexts up to Tmax tiles.
+int page_attn_chunks(int BH, int G, int T);
+int page_attn_chunks_bound(int BH, int G, int Tmax);
+sfi_status check_quant(const sfi_quant_kv* q);
+sfi_status check_index(const sfi_block_index* ix);
 
 }  // namespace sfi

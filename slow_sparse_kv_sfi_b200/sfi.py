@@ -65,6 +65,19 @@ class DenseExtras(C.Structure):
                 ("cand_hi", C.c_int32)]
 
 
+FMT_E4M3, FMT_INT8 = 0, 1
+
+
+class QuantKV(C.Structure):
+    _fields_ = [("k_pool", C.c_void_p), ("v_pool", C.c_void_p), ("k_scale", C.c_void_p), ("v_scale", C.c_void_p),
+                ("k_tail", C.c_void_p), ("v_tail", C.c_void_p), ("page_table", C.c_void_p), ("err", C.c_void_p),
+                ("format", C.c_int32)]
+
+
+class BlockIndex(C.Structure):
+    _fields_ = [("bounds", C.c_void_p), ("scale", C.c_void_p), ("page_table", C.c_void_p), ("err", C.c_void_p)]
+
+
 def _declare(L):
     P, I32, I64, SZ = C.c_void_p, C.c_int32, C.c_int64, C.c_size_t
     sig = {
@@ -88,6 +101,16 @@ def _declare(L):
         "sfi_compact": (C.c_int, [P, P, P, I32, P, I32, I32, P, P, SZ, P]),
         "sfi_compact_incremental": (C.c_int, [P, P, P, I32, P, I32, I32, P, I32, P, SZ, P]),
         "sfi_poll_error": (C.c_int, [P, C.POINTER(I32)]),
+        "sfi_quant_store": (C.c_int, [P, P, P, P, I32, I32, P, P]),
+        "sfi_quant_append": (C.c_int, [P, P, P, I32, P, P, P, P]),
+        "sfi_quant_load": (C.c_int, [P, P, P, I32, I32, P, P]),
+        "sfi_quant_attn": (C.c_int, [P, P, I32, P, P, P, P, P, SZ, P]),
+        "sfi_quant_poll_error": (C.c_int, [P, C.POINTER(I32)]),
+        "sfi_block_build": (C.c_int, [P, P, P, I32, I32, P, P]),
+        "sfi_block_workspace_size": (C.c_int, [P, C.POINTER(SZ)]),
+        "sfi_block_select": (C.c_int, [P, P, I32, P, P, I32, I32, I32, P, I32, P, SZ, P]),
+        "sfi_block_attn": (C.c_int, [P, P, I32, P, P, P, I32, I32, P, P, P, SZ, P]),
+        "sfi_quant_block_attn": (C.c_int, [P, P, I32, P, P, P, I32, I32, P, P, P, SZ, P]),
         "sfi_set_wait_limit": (C.c_int, [C.c_int64]),
         "sfi_get_wait_limit": (C.c_int, [C.POINTER(C.c_int64)]),
         "sfi_selftest_wait": (C.c_int, [P, C.c_int64, P]),
@@ -115,6 +138,9 @@ EXPORTED = ["sfi_status_str", "sfi_version", "sfi_workspace_size", "sfi_packed_r
             "sfi_select_scores", "sfi_topk_workspace_size", "sfi_topk", "sfi_select", "sfi_compact",
             "sfi_compact_incremental", "sfi_poll_error", "sfi_set_wait_limit", "sfi_get_wait_limit",
             "sfi_selftest_wait",
+            "sfi_quant_store", "sfi_quant_append", "sfi_quant_load", "sfi_quant_attn", "sfi_quant_poll_error",
+            "sfi_block_build", "sfi_block_workspace_size", "sfi_block_select", "sfi_block_attn",
+            "sfi_quant_block_attn",
             "sfi_ctx_create", "sfi_ctx_destroy", "sfi_ctx_workspace_size", "sfi_ctx_set_workspace",
             "sfi_decode_step", "sfi_decode_step_rows", "sfi_ctx_join", "sfi_ctx_set_timing", "sfi_ctx_set_timing_layers", "sfi_ctx_set_compaction",
             "sfi_ctx_timing"]
@@ -159,6 +185,80 @@ def make_kv(k_pool, v_pool, page_table, key_norms=None, err=None) -> PagedKV:
 def make_packed(k, v, pos, headmask, n_rows) -> Packed:
     return Packed(k.data_ptr(), v.data_ptr(), pos.data_ptr(), headmask.data_ptr(),
                   n_rows.data_ptr(), k.shape[2])
+
+
+def _arg(t, name, dtypes, shape=None):
+    """Checks a tensor argument of the 8-bit and block calls and returns its address."""
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {' or '.join(str(d) for d in dtypes)}")
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name}: must be on the current CUDA device, is on {t.device}")
+    return C.c_void_p(t.data_ptr())
+
+
+_BF16, _F32, _I32 = (torch.bfloat16,), (torch.float32,), (torch.int32,)
+_CODES = (torch.uint8, torch.int8, torch.float8_e4m3fn)
+
+
+def make_quant_kv(k_pool, v_pool, k_scale, v_scale, k_tail, v_tail, page_table, fmt, err=None) -> QuantKV:
+    """k_pool, v_pool: 8-bit [num_pages, Hkv, 16, D]; scales: fp32 [num_pages, Hkv]; tails: bf16
+    [B, Hkv, 16, D]; page_table: int32 [B, max_pages]; fmt: FMT_E4M3 or FMT_INT8.  The caller keeps the
+    tensors alive."""
+    n, hkv, rows, d = k_pool.shape
+    b, max_pages = page_table.shape
+    if rows != 16:
+        raise ValueError("k_pool: pages have 16 rows")
+    tail = (b, hkv, 16, d)
+    kv = QuantKV(_arg(k_pool, "k_pool", _CODES), _arg(v_pool, "v_pool", _CODES, (n, hkv, 16, d)),
+                 _arg(k_scale, "k_scale", _F32, (n, hkv)), _arg(v_scale, "v_scale", _F32, (n, hkv)),
+                 _arg(k_tail, "k_tail", _BF16, tail), _arg(v_tail, "v_tail", _BF16, tail),
+                 _arg(page_table, "page_table", _I32), None if err is None else _arg(err, "err", _I32, (1,)), fmt)
+    kv.dims = (b, hkv, d, max_pages, n)
+    return kv
+
+
+def make_block_index(bounds, scale, page_table, err=None) -> BlockIndex:
+    """bounds: int8 [num_pages, Hkv, 2, D]; scale: fp32 [num_pages, Hkv]; page_table: int32 [B, max_pages]."""
+    n, hkv, two, d = bounds.shape
+    b, max_pages = page_table.shape
+    if two != 2:
+        raise ValueError("bounds: an upper and a lower bound per page and head")
+    ix = BlockIndex(_arg(bounds, "bounds", (torch.int8,)), _arg(scale, "scale", _F32, (n, hkv)),
+                    _arg(page_table, "page_table", _I32), None if err is None else _arg(err, "err", _I32, (1,)))
+    ix.dims = (b, hkv, d, max_pages, n)
+    return ix
+
+
+def _dims(shape, *parts):
+    """The layer's sizes are those its 8-bit cache and block index were made with."""
+    want = (shape.B, shape.Hkv, shape.D, shape.max_pages, shape.num_pages)
+    for x in parts:
+        if x is not None and getattr(x, "dims", want) != want:
+            raise ValueError(f"{type(x).__name__} has (B, Hkv, D, max_pages, num_pages) {x.dims}, the shape {want}")
+
+
+def _lens(shape, lens):
+    return None if lens is None else _arg(lens, "lens", _I32, (shape.B,))
+
+
+def _attn_args(shape, q, out, lse):
+    qs = (shape.B, shape.Hq, shape.D)
+    return (_arg(q, "q", _BF16, qs), _arg(out, "out", _F32, qs),
+            None if lse is None else _arg(lse, "lse", _F32, qs[:2]))
+
+
+def _sel(shape, sel):
+    if sel.dim() != 3 or sel.shape[0] != shape.B or sel.shape[1] != shape.Hkv:
+        raise ValueError(f"sel: shape {tuple(sel.shape)}, expected ({shape.B}, {shape.Hkv}, at least K)")
+    return _arg(sel, "sel", _I32)
+
+
+def _ws(ws):
+    return _arg(ws, "ws", (ws.dtype,)), ws.numel() * ws.element_size()
 
 
 # ---------------------------------------------------------------- entry points
@@ -289,6 +389,75 @@ def sfi_get_wait_limit() -> int:
 
 def sfi_selftest_wait(kv, limit_ns: int, stream=None):
     _check(lib().sfi_selftest_wait(C.byref(kv), int(limit_ns), _stream(stream)), "sfi_selftest_wait")
+
+
+# ---------------------------------------------------------------- 8-bit cache, block-sparse attention
+def sfi_quant_store(shape, kv, qkv, pos_lo, L, lens=None, index=None, stream=None):
+    _dims(shape, qkv, index)
+    _check(lib().sfi_quant_store(C.byref(shape), C.byref(kv), C.byref(qkv), _ref(index), pos_lo, L,
+                                 _lens(shape, lens), _stream(stream)), "sfi_quant_store")
+
+
+def sfi_quant_append(shape, qkv, L, k_new, v_new, lens=None, index=None, stream=None):
+    _dims(shape, qkv, index)
+    tok = (shape.B, shape.Hkv, shape.D)
+    _check(lib().sfi_quant_append(C.byref(shape), C.byref(qkv), _ref(index), L, _lens(shape, lens),
+                                  _arg(k_new, "k_new", _BF16, tok), _arg(v_new, "v_new", _BF16, tok),
+                                  _stream(stream)), "sfi_quant_append")
+
+
+def sfi_quant_load(shape, qkv, kv, pos_lo, L, lens=None, stream=None):
+    _dims(shape, qkv)
+    _check(lib().sfi_quant_load(C.byref(shape), C.byref(qkv), C.byref(kv), pos_lo, L, _lens(shape, lens),
+                                _stream(stream)), "sfi_quant_load")
+
+
+def sfi_quant_attn(shape, qkv, L, q, out, ws, lens=None, lse=None, stream=None):
+    _dims(shape, qkv)
+    q, out, lse = _attn_args(shape, q, out, lse)
+    _check(lib().sfi_quant_attn(C.byref(shape), C.byref(qkv), L, _lens(shape, lens), q, out, lse, *_ws(ws),
+                                _stream(stream)), "sfi_quant_attn")
+
+
+def sfi_quant_poll_error(qkv) -> int:
+    code = C.c_int32(0)
+    _check(lib().sfi_quant_poll_error(C.byref(qkv), C.byref(code)), "sfi_quant_poll_error")
+    return code.value
+
+
+def sfi_block_build(shape, kv, index, pos_lo, L, lens=None, stream=None):
+    _dims(shape, index)
+    _check(lib().sfi_block_build(C.byref(shape), C.byref(kv), C.byref(index), pos_lo, L, _lens(shape, lens),
+                                 _stream(stream)), "sfi_block_build")
+
+
+def sfi_block_workspace_size(shape: Shape) -> int:
+    n = C.c_size_t(0)
+    _check(lib().sfi_block_workspace_size(C.byref(shape), C.byref(n)), "sfi_block_workspace_size")
+    return n.value
+
+
+def sfi_block_select(shape, index, L, q, n_sink, n_recent, K, sel, ws, lens=None, stream=None):
+    """sel: int32 [B, Hkv, at least K]."""
+    _dims(shape, index)
+    q = _arg(q, "q", _BF16, (shape.B, shape.Hq, shape.D))
+    _check(lib().sfi_block_select(C.byref(shape), C.byref(index), L, _lens(shape, lens), q, n_sink, n_recent, K,
+                                  _sel(shape, sel), sel.shape[-1], *_ws(ws), _stream(stream)), "sfi_block_select")
+
+
+def sfi_block_attn(shape, kv, L, q, sel, K, out, ws, lens=None, lse=None, stream=None):
+    """Attention over blocks sel[:, :, :K] of the bf16 cache."""
+    q, out, lse = _attn_args(shape, q, out, lse)
+    _check(lib().sfi_block_attn(C.byref(shape), C.byref(kv), L, _lens(shape, lens), q, _sel(shape, sel),
+                                sel.shape[-1], K, out, lse, *_ws(ws), _stream(stream)), "sfi_block_attn")
+
+
+def sfi_quant_block_attn(shape, qkv, L, q, sel, K, out, ws, lens=None, lse=None, stream=None):
+    """sfi_block_attn on the 8-bit cache."""
+    _dims(shape, qkv)
+    q, out, lse = _attn_args(shape, q, out, lse)
+    _check(lib().sfi_quant_block_attn(C.byref(shape), C.byref(qkv), L, _lens(shape, lens), q, _sel(shape, sel),
+                                      sel.shape[-1], K, out, lse, *_ws(ws), _stream(stream)), "sfi_quant_block_attn")
 
 
 class Context:
