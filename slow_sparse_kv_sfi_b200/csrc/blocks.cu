@@ -163,11 +163,12 @@ __global__ void __launch_bounds__(kScoreWarps * 32) block_score_kernel(const Blo
 
 BlockWs block_ws(const sfi_shape& s) {
   BlockWs w{};
-  const int BH = s.B * s.Hkv, G = s.Hq / s.Hkv;
+  const long long BH = (long long)s.B * s.Hkv;
+  const int G = s.Hq / s.Hkv;
   size_t off = 0;
   w.score_off = off;
-  off += align_up((size_t)BH * ((s.max_pages + 3) / 4 * 4) * sizeof(float), 256);
-  const size_t items = (size_t)BH * page_attn_chunks_bound(BH, G, s.max_pages);
+  off += align_up((size_t)BH * (((size_t)s.max_pages + 3) / 4 * 4) * sizeof(float), 256);
+  const size_t items = 2 * (size_t)page_attn_ctas(BH * s.max_pages, 2);
   w.part_off = off;
   off += align_up(items * G * s.D * sizeof(float), 256);
   w.ml_off = off;

@@ -204,10 +204,9 @@ struct BlockWs {
   size_t score_off, part_off, ml_off, total;
 };
 BlockWs block_ws(const sfi_shape& s);
-// Chunks per (sequence, KV head) that sfi_block_attn and its kin cut T tiles
-// into, and its largest value over contexts up to Tmax tiles.
-int page_attn_chunks(int BH, int G, int T);
-int page_attn_chunks_bound(int BH, int G, int Tmax);
+// CTAs of an attention launch over this many tiles, at most per_sm on each
+// multiprocessor (pattn.cu); it leaves two partials per CTA.
+int page_attn_ctas(long long tiles, int per_sm);
 sfi_status check_quant(const sfi_quant_kv* q);
 sfi_status check_index(const sfi_block_index* ix);
 

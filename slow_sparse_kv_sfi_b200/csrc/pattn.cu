@@ -3,11 +3,14 @@
 //
 //   z_j = q . k_j / sqrt(D),  out = sum_j softmax(z)_j v_j
 //
-// Work.  The pages (or list entries) of one (sequence, KV head) are cut into
-// chunks, one CTA each; warp w of the CTA takes tiles w, w + W, ... of its
-// chunk, a tile being one page: 16 rows of K and of V.  Each warp runs its own
-// online softmax; the CTA merges its warps in shared memory, and a second
-// kernel merges the chunks.
+// Work.  A tile is one page: 16 rows of K and of V.  The tiles of all rows - a
+// row being one (sequence, KV head), its tiles its pages or list entries - form
+// one sequence, and every CTA takes an equal run of it, whatever the lengths;
+// the grid is what the GPU holds at once.  A run cuts at most two rows: a row
+// inside one run is finished there, the pieces of the others are merged by a
+// second kernel.  Within a row, warp w of the CTA takes tiles w, w + W, ...;
+// each warp runs its own online softmax and the CTA merges its warps in shared
+// memory.
 //
 // Bound by reading the cache, so the layout serves the loads.  Every warp
 // streams its tiles through its own ring of stages with 16-byte asynchronous
@@ -21,11 +24,14 @@
 //   O^T[D x 8 heads] += V^T[D x 16] . P^T[16 x 8]: it holds tokens 2t, 2t + 1,
 //     2t + 8, 2t + 9 and a run of D / 8 columns of each; two tokens' bytes are
 //     interleaved into the 16-bit pairs that the fragment wants.
-// 8-bit codes become bf16 in registers, exactly (int8 and e4m3 both fit); the
-// key scale multiplies the logits, the value scale the probabilities.
-// P is split into bf16 hi + lo, which keeps about 16 bits of it.
-// The running maximum moves only when a logit exceeds it by 6 (P up to 64, far
-// from overflow), so most tiles need no rescaling and no reduction.
+// 8-bit codes become fp16 in registers, exactly (int8 and e4m3 both fit), and Q
+// fp16 times a power of two per head; the key scale multiplies the logits, the
+// value scale the tile's product.  P is split into hi + lo, which keeps 22 bits
+// of it in fp16 (8-bit pages) and 16 in bf16 (bf16 rows, whose range fp16 lacks).
+// The softmax reference moves only when a logit exceeds it by a margin, so most
+// tiles need no rescaling and no reduction.
+#include <cuda_fp16.h>
+
 #include <algorithm>
 
 #include "common.cuh"
@@ -35,7 +41,11 @@ namespace sfi {
 namespace {
 
 constexpr int kBf16 = 2;            // FMT: SFI_FMT_E4M3, SFI_FMT_INT8 or this
-constexpr float kSlack = 6.f;       // log2 of the largest P
+// A warp's reference m is set kBias below its largest logit so far (log2 units)
+// and moves when a logit exceeds it by kBias + kSlack: P reaches 2^14, inside
+// fp16, and is held to 2^-24 * 2^-8 of the largest one below that.
+constexpr float kBias = 8.f, kSlack = 6.f;
+constexpr float kNoMax = -3.4028234663852886e38f;   // m before the first logit
 
 struct PageAttnArgs {
   int B, Hq, Hkv, G, L, num_pages, max_pages;
@@ -51,36 +61,126 @@ struct PageAttnArgs {
   const int32_t* sel;               // LIST
   int64_t sel_ld;
   int K;
-  int chunk;                        // tiles per chunk
-  int n_chunks;
+  int ctas;                         // of the grid
   float scale_log2;                 // log2(e) / sqrt(D)
   float* out;
   float* lse;
-  float* part;                      // [item][G][D]
-  float* ml;                        // [item][G][2]
+  float* part;                      // [cta][2][G][D]: piece of the row that began before, that goes on behind
+  float* ml;                        // [cta][2][G][2]
   int* err;
 };
 
-template <int D, int FMT, int NT>
+// HM, how the group's heads fill the 8 columns of a product: kHalf (G <= 4) has
+// heads 0 .. 3 twice, the second time with the low part of P, so one product
+// serves both parts; kOne (G <= 8) and kTwo (G <= 16) take hi and lo in turn.
+#ifndef PA_TP
+#define PA_TP 2
+#endif
+#ifndef PA_W
+#define PA_W 6
+#endif
+#ifndef PA_S
+#define PA_S 2
+#endif
+#ifndef PA_MINQ
+#define PA_MINQ 12
+#endif
+enum HeadMap : int { kHalf = 0, kOne = 1, kTwo = 2 };
+
+template <int D, int FMT, int HM>
 struct Cfg {
+  static constexpr int NT = HM == kTwo ? 2 : 1;         // column tiles
   static constexpr int kEl = FMT == kBf16 ? 2 : 1;
   static constexpr int kRow = D * kEl;                  // bytes of a row
   static constexpr int KJ = kRow / 64;                  // 16-byte chunks of a K row per thread
   static constexpr int kVB = kRow / 8;                  // bytes of a V row per thread: 8, 16 or 32
   static constexpr int VC = kVB >= 16 ? kVB / 16 : 1;   // pieces of them
   static constexpr int VP = kVB >= 16 ? 16 : 8;         // bytes of a piece
-  static constexpr int kKBytes = 16 * kRow;             // of a stage, K and V alike
-  static constexpr int kStage = 2 * kKBytes;
-  // Warps and stages: about 96 KB of copies in flight per SM at two CTAs (one
-  // for G > 8, whose accumulators need twice the registers).
-  static constexpr int W = FMT == kBf16 ? 4 : 8;
+  static constexpr int kKBytes = 16 * kRow;             // of a tile, K and V alike
+  static constexpr int kTile = 2 * kKBytes;
+  // A step is TP tiles, a stage holds one step.
+  static constexpr int TP = FMT == kBf16 ? 1 : PA_TP;
+  static constexpr int W = FMT == kBf16 ? 4 : PA_W;
   static constexpr int kCtas = NT == 1 ? 2 : 1;
-  static constexpr int S = D == 64 ? 4 : 3;
+  static constexpr int kStage = TP * kTile;
+  static constexpr int S = FMT == kBf16 ? 3 : PA_S;
   static constexpr int kRing = W * S * kStage;
   static constexpr int kMerge = W * NT * 8 * (D + 8) * 4 + W * NT * 8 * 2 * 4;
-  static constexpr int kMeta = W * S * 16;
+  static constexpr int kMeta = W * S * TP * 16;
   static constexpr int kSmem = (kRing > kMerge ? kRing : kMerge) + kMeta;
 };
+
+// The run of each CTA is `quota` tiles of the whole sequence.
+constexpr int kMinQuota = PA_MINQ;   // a smaller run would not fill the warps of a CTA
+__host__ __device__ __forceinline__ long long quota(long long total, int ctas) {
+  const long long q = (total + ctas - 1) / ctas;
+  return q > kMinQuota ? q : kMinQuota;
+}
+
+// Tiles of a row of sequence b.
+template <bool LIST>
+__device__ __forceinline__ int row_tiles(const PageAttnArgs& a, int b, int* err) {
+  return LIST ? a.K : (seq_len(a.lens, a.L, b, err) + kPage - 1) / kPage;
+}
+
+// Tiles of all rows, and of the rows of sequences before b (one warp; all
+// lanes get both).
+template <bool LIST>
+__device__ __forceinline__ void count_tiles(const PageAttnArgs& a, int b, int lane, int* err, long long& total,
+                                            long long& before) {
+  if (LIST || !a.lens) {
+    const long long per = (long long)row_tiles<LIST>(a, 0, err) * a.Hkv;
+    total = per * a.B;
+    before = per * b;
+    return;
+  }
+  long long t = 0, p = 0;
+  for (int i = lane; i < a.B; i += 32) {
+    const long long v = (long long)row_tiles<LIST>(a, i, err) * a.Hkv;
+    t += v;
+    if (i < b) p += v;
+  }
+#pragma unroll
+  for (int sh = 16; sh >= 1; sh >>= 1) {
+    t += __shfl_xor_sync(0xffffffffu, t, sh);
+    p += __shfl_xor_sync(0xffffffffu, p, sh);
+  }
+  total = t;
+  before = p;
+}
+
+// The sequence whose rows hold tile `pos` (< total) and the first tile of its
+// rows (one warp; all lanes get both).
+template <bool LIST>
+__device__ __forceinline__ void find_sequence(const PageAttnArgs& a, long long pos, int lane, int& b, long long& first) {
+  if (LIST || !a.lens) {
+    const long long per = (long long)row_tiles<LIST>(a, 0, nullptr) * a.Hkv;
+    b = (int)(pos / per);
+    first = per * b;
+    return;
+  }
+  long long base = 0;
+  for (int i0 = 0; i0 < a.B; i0 += 32) {
+    const int i = i0 + lane;
+    const long long v = i < a.B ? (long long)row_tiles<LIST>(a, i, nullptr) * a.Hkv : 0;
+    long long x = v;
+#pragma unroll
+    for (int sh = 1; sh < 32; sh <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, x, sh);
+      if (lane >= sh) x += y;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, base + x > pos);
+    if (hit) {
+      const int l = __ffs(hit) - 1;
+      b = i0 + l;
+      first = base + __shfl_sync(0xffffffffu, x - v, l);
+      return;
+    }
+    base += __shfl_sync(0xffffffffu, x, 31);
+  }
+  b = a.B;   // not reached for pos < total
+  first = base;
+}
 
 struct Meta {       // of a stage
   int page;         // >= 0; -1: nothing; -2: the tail
@@ -105,83 +205,141 @@ __device__ __forceinline__ void cp_wait() {
 __device__ __forceinline__ uint4 lds16(const uint8_t* p) { return *reinterpret_cast<const uint4*>(p); }
 __device__ __forceinline__ uint2 lds8(const uint8_t* p) { return *reinterpret_cast<const uint2*>(p); }
 
-// Bytes 0, 2 of v -> ev and bytes 1, 3 -> od, as bf16 pairs.
-//  int8: x = low7 - 128 s (s the sign bit); 0x4300 | low7 is 128 + low7 and
-//        0x4300 | 0x80 s is 128 + 128 s in bf16, so their difference is x.
-//  e4m3: sign, exponent and mantissa bits moved to their bf16 places are the
-//        value times 2^(7 - 127), subnormals included; times 2^120.
-template <int FMT>
-__device__ __forceinline__ void to_bf16(uint32_t v, uint32_t& ev, uint32_t& od) {
-  if constexpr (FMT == SFI_FMT_INT8) {
-    const uint32_t o = v >> 8;
-    const uint32_t a = (v & 0x007f007fu) | 0x43004300u, b = (v & 0x00800080u) | 0x43004300u;
-    const uint32_t c = (o & 0x007f007fu) | 0x43004300u, d = (o & 0x00800080u) | 0x43004300u;
-    const __nv_bfloat162 e = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
-    const __nv_bfloat162 f = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&c), *reinterpret_cast<const __nv_bfloat162*>(&d));
-    ev = *reinterpret_cast<const uint32_t*>(&e);
-    od = *reinterpret_cast<const uint32_t*>(&f);
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ float2 unpack_f16x2(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2*>(&v)); }
+
+// D += A * B, m16n8k16, fp16 inputs, fp32 accumulate.
+__device__ __forceinline__ void mma_f16_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// D += A * B, or D = A * B.
+template <bool F16, bool ADD>
+__device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (ADD) {
+    if constexpr (F16) mma_f16_16816(d, a, b0, b1);
+    else mma_bf16_16816(d, a, b0, b1);
+  } else if constexpr (F16) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
   } else {
-    const uint32_t a = ((v << 4) & 0x07f007f0u) | ((v << 8) & 0x80008000u);
-    const uint32_t b = ((v >> 4) & 0x07f007f0u) | (v & 0x80008000u);
-    const uint32_t m = 0x7b807b80u;   // 2^120, twice
-    const __nv_bfloat162 k = *reinterpret_cast<const __nv_bfloat162*>(&m);
-    const __nv_bfloat162 e = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&a), k);
-    const __nv_bfloat162 f = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&b), k);
-    ev = *reinterpret_cast<const uint32_t*>(&e);
-    od = *reinterpret_cast<const uint32_t*>(&f);
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+  }
+}
+
+// Codes in bytes 0, 1 of v -> lo and bytes 2, 3 -> hi, as fp16 pairs, exactly.
+// e4m3: the hardware conversion.  int8: x + 128 in the low byte of 0x6400 is
+// 1024 + 128 + x in fp16, less 1152.
+template <int FMT>
+__device__ __forceinline__ void to_f16(uint32_t v, uint32_t& lo, uint32_t& hi) {
+  if constexpr (FMT == SFI_FMT_INT8) {
+    const uint32_t u = v ^ 0x80808080u;
+    const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+    const __half2 k = __float2half2_rn(1152.f);
+    const __half2 e = __hsub2(*reinterpret_cast<const __half2*>(&a), k);
+    const __half2 f = __hsub2(*reinterpret_cast<const __half2*>(&b), k);
+    lo = *reinterpret_cast<const uint32_t*>(&e);
+    hi = *reinterpret_cast<const uint32_t*>(&f);
+  } else {
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(v));
   }
 }
 
 __device__ __forceinline__ uint32_t word(const uint4& x, int w) { return w == 0 ? x.x : w == 1 ? x.y : w == 2 ? x.z : x.w; }
 
-// The state of one warp: running maximum (log2 units) and this thread's share
-// of the sum for heads 2t, 2t + 1 of each head tile, and O^T.
+// The state of one warp: reference m (log2 units) and this thread's share of
+// the sum for heads 2t, 2t + 1 of each head tile, and O^T in units of vref.
 template <int D, int NT>
 struct State {
   float o[NT][D / 16][4];
   float m[NT][2], l[NT][2];
+  float vref, vinv;   // and 1 / vref
 };
 
-// One tile from its fragments: kf(step, a[4]) and vf(step, a[4]) fill the A
-// operands of S^T and O^T.  rows: valid rows of the tile.
-template <int D, int NT, class KF, class VF>
-__device__ __forceinline__ void tile_math(State<D, NT>& st, const uint32_t (&qb)[NT][D / 16][2], float zf, float vs,
-                                          int rows, int lane, KF kf, VF vf) {
-  float s[NT][4], s2[NT][4];
+template <int D, int NT>
+__device__ __forceinline__ void scale_o(State<D, NT>& st, float f) {
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s[nt][i] = s2[nt][i] = 0.f;
+    for (int k = 0; k < D / 16; ++k)
 #pragma unroll
-  for (int k = 0; k < D / 16; k += 2) {
-    uint32_t a[4], b[4];
-    kf(k, a);
-    kf(k + 1, b);
+      for (int i = 0; i < 4; ++i) st.o[nt][k][i] *= f;
+}
+
+// TP tiles from their fragments: kf(tile, step, a) and vf(tile, step, a) fill
+// the A operands of S^T and O^T, qf(column tile, step, b0, b1) the B operand of
+// S^T; vload() runs between the two products.  zf: log2 units per unit of S^T,
+// per tile and head; vs: the value scales; rows: valid rows (0: no tile).
+// F16: fp16 operands (8-bit pages), else bf16.  SCALED: the cache has value
+// scales.
+template <int D, int HM, bool F16, bool SCALED, int TP, class KF, class QF, class VL, class VF, int NT>
+__device__ __forceinline__ void tile_math(State<D, NT>& st, const float (&zf)[TP][NT][2], const float (&vs)[TP],
+                                          const int (&rows)[TP], int lane, KF kf, QF qf, VL vload, VF vf) {
+  float s[TP][NT][4], x[TP][NT][4];
+#pragma unroll
+  for (int k = 0; k < D / 16; ++k) {
+    uint32_t a[TP][4];
+#pragma unroll
+    for (int u = 0; u < TP; ++u) kf(u, k, a[u]);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      mma_bf16_16816(s[nt], a, qb[nt][k][0], qb[nt][k][1]);
-      mma_bf16_16816(s2[nt], b, qb[nt][k + 1][0], qb[nt][k + 1][1]);
+      uint32_t b0, b1;
+      qf(nt, k, b0, b1);
+#pragma unroll
+      for (int u = 0; u < TP; ++u) {
+        if (k == 0) mma16<F16, false>(s[u][nt], a[u], b0, b1);
+        else if (k == 1) mma16<F16, false>(x[u][nt], a[u], b0, b1);
+        else if (k % 2 == 0) mma16<F16, true>(s[u][nt], a[u], b0, b1);
+        else mma16<F16, true>(x[u][nt], a[u], b0, b1);
+      }
     }
   }
+  vload();
   bool grow = false;
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
+  for (int u = 0; u < TP; ++u)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      s[nt][i] = (s[nt][i] + s2[nt][i]) * zf;
-      if (rows < kPage && (lane >> 2) + 8 * (i >> 1) >= rows) s[nt][i] = -INFINITY;
-      grow |= s[nt][i] > st.m[nt][i & 1] + kSlack;
-    }
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        s[u][nt][i] += x[u][nt][i];
+        // one rounding, of the difference; no tile: s is 0
+        x[u][nt][i] = fmaf(s[u][nt][i], zf[u][nt][i & 1], TP > 1 && rows[u] == 0 ? -INFINITY : -st.m[nt][i & 1]);
+        if (TP == 1 && rows[u] < kPage && (lane >> 2) + 8 * (i >> 1) >= rows[u]) x[u][nt][i] = -INFINITY;
+        grow |= x[u][nt][i] > kBias + kSlack;
+      }
   if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        float x = fmaxf(s[nt][j], s[nt][j + 2]);
+        float z = -INFINITY;
 #pragma unroll
-        for (int sh = 4; sh <= 16; sh <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, sh));
-        const float mn = fmaxf(st.m[nt][j], x);
-        const float al = mn == -INFINITY ? 1.f : fast_exp2(st.m[nt][j] - mn);
+        for (int u = 0; u < TP; ++u)
+#pragma unroll
+          for (int r = 0; r < 2; ++r)
+            if (x[u][nt][j + 2 * r] != -INFINITY) z = fmaxf(z, s[u][nt][j + 2 * r] * zf[u][nt][j]);
+#pragma unroll
+        for (int sh = 4; sh <= 16; sh <<= 1) z = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, sh));
+        const float mn = fmaxf(st.m[nt][j], z - kBias);
+        const float al = fast_exp2(st.m[nt][j] - mn);
         st.m[nt][j] = mn;
         st.l[nt][j] *= al;
 #pragma unroll
@@ -189,80 +347,157 @@ __device__ __forceinline__ void tile_math(State<D, NT>& st, const uint32_t (&qb)
           st.o[nt][k][j] *= al;
           st.o[nt][k][j + 2] *= al;
         }
+#pragma unroll
+        for (int u = 0; u < TP; ++u)
+#pragma unroll
+          for (int r = 0; r < 2; ++r)
+            if (x[u][nt][j + 2 * r] != -INFINITY)
+              x[u][nt][j + 2 * r] = fmaf(s[u][nt][j + 2 * r], zf[u][nt][j], -mn);
       }
   }
-  uint32_t hi[NT][2], lo[NT][2];
+  // The value scale multiplies P, relative to vref so that fp16 holds it: vref
+  // follows the largest scale seen (within a factor of 2); a page whose scale
+  // is 2^6 and more below it, which fp16 would hold less exactly, has its
+  // product scaled instead.
+  float pv[TP];
+  bool apart = false;
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
+  for (int u = 0; u < TP; ++u) pv[u] = 1.f;
+  if constexpr (SCALED) {
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      float p[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const float m = st.m[nt][j] == -INFINITY ? 0.f : st.m[nt][j];
-        p[j] = fast_exp2(s[nt][2 * r + j] - m);
-        st.l[nt][j] += p[j];
-        p[j] *= vs;
+    for (int u = 0; u < TP; ++u)
+      if (!(vs[u] <= 2.f * st.vref)) {   // NaN too
+        scale_o(st, __fdiv_rn(st.vref, vs[u]));
+        st.vref = vs[u];
+        st.vinv = __fdiv_rn(1.f, vs[u]);
       }
-      const uint32_t h = pack_bf16x2(p[0], p[1]);
-      const float2 f = unpack_bf16x2(h);
-      hi[nt][r] = movmatrix_trans(h);
-      lo[nt][r] = movmatrix_trans(pack_bf16x2(p[0] - f.x, p[1] - f.y));
-    }
 #pragma unroll
-  for (int k = 0; k < D / 16; ++k) {
-    uint32_t a[4];
-    vf(k, a);
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      mma_bf16_16816(st.o[nt][k], a, hi[nt][0], hi[nt][1]);
-      mma_bf16_16816(st.o[nt][k], a, lo[nt][0], lo[nt][1]);
+    for (int u = 0; u < TP; ++u) {
+      pv[u] = vs[u] * st.vinv;
+      apart |= F16 && pv[u] < 0.015625f && rows[u] > 0;
     }
+  }
+  apart = SCALED && F16 && __any_sync(0xffffffffu, apart);   // the same in every lane; a vote lets the compiler branch
+  uint32_t hi[TP][NT][2], lo[TP][NT][2];
+#pragma unroll
+  for (int u = 0; u < TP; ++u)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        float p0 = fast_exp2(x[u][nt][2 * r]), p1 = fast_exp2(x[u][nt][2 * r + 1]);
+        st.l[nt][0] += p0;
+        st.l[nt][1] += p1;
+        if constexpr (SCALED) {
+          const float f = apart ? 1.f : pv[u];
+          p0 *= f;
+          p1 *= f;
+        }
+        const uint32_t h = F16 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
+        const float2 f = F16 ? unpack_f16x2(h) : unpack_bf16x2(h);
+        const uint32_t q = F16 ? pack_f16x2(p0 - f.x, p1 - f.y) : pack_bf16x2(p0 - f.x, p1 - f.y);
+        if constexpr (HM == kHalf) {
+          hi[u][nt][r] = movmatrix_trans((lane & 2) ? q : h);
+        } else {
+          hi[u][nt][r] = movmatrix_trans(h);
+          lo[u][nt][r] = movmatrix_trans(q);
+        }
+      }
+  if (SCALED && F16 && apart) {
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+      for (int u = 0; u < TP; ++u) {
+        uint32_t a[4];
+        vf(u, k, a);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float c[4];
+          mma16<F16, false>(c, a, hi[u][nt][0], hi[u][nt][1]);
+          if constexpr (HM != kHalf) mma16<F16, true>(c, a, lo[u][nt][0], lo[u][nt][1]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) st.o[nt][k][i] = fmaf(pv[u], c[i], st.o[nt][k][i]);
+        }
+      }
+  } else {
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+      for (int u = 0; u < TP; ++u) {
+        uint32_t a[4];
+        vf(u, k, a);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          mma16<F16, true>(st.o[nt][k], a, hi[u][nt][0], hi[u][nt][1]);
+          if constexpr (HM != kHalf) mma16<F16, true>(st.o[nt][k], a, lo[u][nt][0], lo[u][nt][1]);
+        }
+      }
   }
 }
 
-template <int D, int FMT, int NT, bool LIST>
-__global__ void __launch_bounds__(Cfg<D, FMT, NT>::W * 32, Cfg<D, FMT, NT>::kCtas)
-    page_attn_kernel(const __grid_constant__ PageAttnArgs a) {
-  using C = Cfg<D, FMT, NT>;
-  constexpr int W = C::W, S = C::S, KJ = C::KJ, VC = C::VC, VP = C::VP;
-  extern __shared__ __align__(16) uint8_t smem[];
+// Tiles [t0, t1) of the T tiles of row (b, h), by the whole CTA: the row's
+// output, or (not the whole row) its piece for the merge.
+template <int D, int FMT, int HM, bool LIST>
+__device__ __forceinline__ void attend_row(const PageAttnArgs& a, uint8_t* smem, int b, int h, int len, int T, int t0,
+                                           int t1) {
+  using C = Cfg<D, FMT, HM>;
+  constexpr int NT = C::NT, TP = C::TP, W = C::W, S = C::S, KJ = C::KJ, VC = C::VC, VP = C::VP;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
-  const int bh = blockIdx.y, b = bh / a.Hkv, h = bh - b * a.Hkv;
-  grid_dep_wait();
-  if (a.n_chunks > 1) grid_dep_launch();
-
-  const int len = seq_len(a.lens, a.L, b, a.err);
+  const int bh = b * a.Hkv + h;
   const int blocks = (len + kPage - 1) / kPage;
-  const int T = LIST ? a.K : blocks;
-  const int t0 = blockIdx.x * a.chunk, t1 = min(T, t0 + a.chunk);
-  if (!LIST && t0 >= T && a.n_chunks > 1) return;   // the merge kernel counts chunks alike
 
   // queries of the group: B operands of S^T, in the column order of the K
-  // fragments (zero for heads past G)
+  // fragments (zero for heads past G).  8-bit pages: fp16, each head times the
+  // power of two that takes its largest value into [2^14, 2^15) (an element
+  // below 2^-39 of that loses bits); zq undoes it.
   uint32_t qb[NT][D / 16][2];
+  float zq[NT][2];
+  auto q_at = [&](int nt, int k) {   // four columns of the head of column nt * 8 + g
+    const int n = HM == kHalf ? g & 3 : nt * 8 + g;
+    const int d = FMT == kBf16 ? (t + 4 * (k / 2)) * 8 + (k % 2) * 4 : (t + 4 * (k / 4)) * 16 + (k % 4) * 4;
+    if (n >= a.G) return make_uint2(0, 0);
+    return __ldg(reinterpret_cast<const uint2*>(a.q + ((size_t)b * a.Hq + h * a.G + n) * D + d));
+  };
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    const int n = nt * 8 + g;
-    const __nv_bfloat16* q = a.q + ((size_t)b * a.Hq + h * a.G + (n < a.G ? n : 0)) * D;
+    uint32_t am = 0;
 #pragma unroll
     for (int k = 0; k < D / 16; ++k) {
-      const int d = FMT == kBf16 ? (t + 4 * (k / 2)) * 8 + (k % 2) * 4 : (t + 4 * (k / 4)) * 16 + (k % 4) * 4;
-      uint2 x = __ldg(reinterpret_cast<const uint2*>(q + d));
-      if (n >= a.G) x = make_uint2(0, 0);
-      qb[nt][k][0] = FMT == kBf16 ? x.x : __byte_perm(x.x, x.y, 0x5410);
-      qb[nt][k][1] = FMT == kBf16 ? x.y : __byte_perm(x.x, x.y, 0x7632);
+      const uint2 x = q_at(nt, k);
+      qb[nt][k][0] = x.x;
+      qb[nt][k][1] = x.y;
+      am = __vmaxu2(am, __vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu));
+    }
+    zq[nt][0] = zq[nt][1] = a.scale_log2;
+    if constexpr (FMT != kBf16) {
+      am = max(am & 0xffffu, am >> 16);
+      am = max(am, __shfl_xor_sync(0xffffffffu, am, 1));
+      am = max(am, __shfl_xor_sync(0xffffffffu, am, 2));
+      // biased exponent of the head's largest value; up = 2^(14 - exponent)
+      const int e = (int)(am >> 7);
+      const int up = e == 0xff || am == 0 ? 127 : min(127 + 14 - (e - 127), 253);
+      const float f = __uint_as_float((uint32_t)up << 23), inv = __uint_as_float((uint32_t)(254 - up) << 23);
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float2 x = unpack_bf16x2(qb[nt][k][i]);
+          qb[nt][k][i] = pack_f16x2(x.x * f, x.y * f);
+        }
+#pragma unroll
+      for (int j = 0; j < 2; ++j) zq[nt][j] *= __shfl_sync(0xffffffffu, inv, (2 * t + j) * 4);
     }
   }
 
   uint8_t* ring = smem + (size_t)warp * S * C::kStage;
   const uint32_t ring_u = smem_u32(ring) + lane * 16;
-  Meta* meta = reinterpret_cast<Meta*>(smem + (C::kSmem - C::kMeta)) + warp * S;
+  Meta* meta = reinterpret_cast<Meta*>(smem + (C::kSmem - C::kMeta)) + warp * S * TP;
 
-  // Tiles of this warp: t0 + warp + W * i, i < n.  Lane l looks up tile
-  // i0 + l of a batch of 32: block, page and scales.
+  // Tiles of this warp: t0 + warp + W * i, i < n, in steps of TP.  Lane l looks
+  // up tile i0 + l of a batch of 32: block, page and scales.
   const int n = t1 - t0 > warp ? (t1 - t0 - warp + W - 1) / W : 0;
+  const int steps = (n + TP - 1) / TP;
   Meta mine{-1, 0, 0.f, 0.f};
   auto look_up = [&](int i0) {
     mine = Meta{-1, 0, 0.f, 0.f};
@@ -279,6 +514,7 @@ __global__ void __launch_bounds__(Cfg<D, FMT, NT>::W * 32, Cfg<D, FMT, NT>::kCta
     const int page = __ldg(a.pt + (size_t)b * a.max_pages + blk);
     if ((unsigned)page >= (unsigned)a.num_pages) {
       latch_error(a.err, SFI_ERR_DEVICE_CHECK, kSitePageAttn);
+      mine.rows = 0;
       return;
     }
     mine.page = page;
@@ -288,18 +524,29 @@ __global__ void __launch_bounds__(Cfg<D, FMT, NT>::W * 32, Cfg<D, FMT, NT>::kCta
     }
   };
 
-  // copies of tile i into stage i % S
+  // copies of step i into stage i % S
   auto issue = [&](int i) {
-    if (i < n) {
-      if ((i & 31) == 0) look_up(i);
-      const int src = i & 31;
-      if (lane == src) meta[i % S] = mine;
-      const int page = __shfl_sync(0xffffffffu, mine.page, src);
-      if (page >= 0) {
+    if (i < steps) {
+      const int first = i * TP;
+      if ((first & 31) == 0) look_up(first);
+      const int st = i % S;
+      if (lane - (first & 31) >= 0 && lane - (first & 31) < TP) meta[st * TP + lane - (first & 31)] = mine;
+#pragma unroll
+      for (int u = 0; u < TP; ++u) {
+        const int src = (first + u) & 31;
+        const int page = __shfl_sync(0xffffffffu, mine.page, src);
+        if (page < 0) {
+          // no tile in this place of the step: zeros, which its mask then drops
+          if (TP > 1)
+#pragma unroll
+            for (int x = 0; x < C::kTile / 512; ++x)
+              *reinterpret_cast<uint4*>(ring + st * C::kStage + u * C::kTile + x * 512 + lane * 16) = make_uint4(0, 0, 0, 0);
+          continue;
+        }
         const size_t off = ((size_t)page * a.Hkv + h) * C::kKBytes;
         const uint8_t* kp = a.k + off + g * C::kRow + t * 16;
         const uint8_t* vp = a.v + off + 2 * t * C::kRow + g * VP;
-        const uint32_t sk = ring_u + (i % S) * C::kStage, sv = sk + C::kKBytes;
+        const uint32_t sk = ring_u + st * C::kStage + u * C::kTile, sv = sk + C::kKBytes;
         if constexpr (FMT == kBf16) {
           const int rows = __shfl_sync(0xffffffffu, mine.rows, src);
 #pragma unroll
@@ -333,11 +580,13 @@ __global__ void __launch_bounds__(Cfg<D, FMT, NT>::W * 32, Cfg<D, FMT, NT>::kCta
   };
 
   State<D, NT> st;
+  st.vref = FMT == kBf16 ? 1.f : 1.17549435e-38f;   // the smallest normal: any scale takes its place
+  st.vinv = FMT == kBf16 ? 1.f : 8.50705917e37f;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      st.m[nt][j] = -INFINITY;
+      st.m[nt][j] = kNoMax;
       st.l[nt][j] = 0.f;
     }
 #pragma unroll
@@ -348,89 +597,137 @@ __global__ void __launch_bounds__(Cfg<D, FMT, NT>::W * 32, Cfg<D, FMT, NT>::kCta
 
 #pragma unroll
   for (int i = 0; i < S - 1; ++i) issue(i);
-  for (int i = 0; i < n; ++i) {
+  auto q_regs = [&](int nt, int k, uint32_t& b0, uint32_t& b1) {
+    b0 = qb[nt][k][0];
+    b1 = qb[nt][k][1];
+  };
+  for (int i = 0; i < steps; ++i) {
     __syncwarp();   // every lane has read stage (i - 1) % S's description
     issue(i + S - 1);
     cp_wait<S - 1>();
     __syncwarp();
-    const Meta mt = meta[i % S];
     const uint8_t* sk = ring + (i % S) * C::kStage + lane * 16;
-    const uint8_t* sv = sk + C::kKBytes;
-    if (mt.page >= 0) {
+    float zf[TP][NT][2], vs[TP];
+    int rows[TP];
+    bool any = false, tail = false;
+    int tail_rows = 0;
+#pragma unroll
+    for (int u = 0; u < TP; ++u) {
+      const Meta mt = meta[(i % S) * TP + u];
+      rows[u] = mt.page >= 0 ? mt.rows : 0;
+      any |= mt.page >= 0;
+      if (mt.page == -2) {
+        tail = true;
+        tail_rows = mt.rows;
+      }
+      vs[u] = mt.vs;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) zf[u][nt][j] = FMT == kBf16 ? a.scale_log2 : zq[nt][j] * mt.ks;
+    }
+    if (any) {
+      uint4 kx[TP][2 * KJ], vx[TP][4 * VC];
+#pragma unroll
+      for (int u = 0; u < TP; ++u)
+#pragma unroll
+        for (int j = 0; j < 2 * KJ; ++j) kx[u][j] = lds16(sk + u * C::kTile + j * 512);
+      auto v_load = [&]() {
+#pragma unroll
+        for (int u = 0; u < TP; ++u) {
+          const uint8_t* sv = sk + u * C::kTile + C::kKBytes;
+#pragma unroll
+          for (int x = 0; x < 4 * VC; ++x) {
+            if constexpr (VP == 16) {
+              vx[u][x] = lds16(sv + x * 512);
+            } else {
+              const uint2 y = lds8(sv - lane * 8 + x * 256);
+              vx[u][x] = make_uint4(y.x, y.y, 0, 0);
+            }
+          }
+        }
+      };
       if constexpr (FMT == kBf16) {
-        tile_math<D, NT>(
-            st, qb, a.scale_log2, 1.f, mt.rows, lane,
-            [&](int k, uint32_t (&f)[4]) {
-              const uint4 x = lds16(sk + (k / 2) * 512), y = lds16(sk + (KJ + k / 2) * 512);
+        tile_math<D, HM, false, false, TP>(
+            st, zf, vs, rows, lane,
+            [&](int u, int k, uint32_t (&f)[4]) {
               const int w = (k % 2) * 2;
-              f[0] = word(x, w);
-              f[1] = word(y, w);
-              f[2] = word(x, w + 1);
-              f[3] = word(y, w + 1);
+              f[0] = word(kx[u][k / 2], w);
+              f[1] = word(kx[u][KJ + k / 2], w);
+              f[2] = word(kx[u][k / 2], w + 1);
+              f[3] = word(kx[u][KJ + k / 2], w + 1);
             },
-            [&](int k, uint32_t (&f)[4]) {
+            q_regs, v_load,
+            [&](int u, int k, uint32_t (&f)[4]) {
               const int c = k / 4, w = k % 4;
-              const uint32_t x0 = word(lds16(sv + c * 512), w), x1 = word(lds16(sv + (VC + c) * 512), w);
-              const uint32_t x2 = word(lds16(sv + (2 * VC + c) * 512), w), x3 = word(lds16(sv + (3 * VC + c) * 512), w);
+              const uint32_t x0 = word(vx[u][c], w), x1 = word(vx[u][VC + c], w);
+              const uint32_t x2 = word(vx[u][2 * VC + c], w), x3 = word(vx[u][3 * VC + c], w);
               f[0] = __byte_perm(x0, x1, 0x5410);
               f[1] = __byte_perm(x0, x1, 0x7632);
               f[2] = __byte_perm(x2, x3, 0x5410);
               f[3] = __byte_perm(x2, x3, 0x7632);
             });
       } else {
-        tile_math<D, NT>(
-            st, qb, a.scale_log2 * mt.ks, mt.vs, kPage, lane,
-            [&](int k, uint32_t (&f)[4]) {
-              to_bf16<FMT>(word(lds16(sk + (k / 4) * 512), k % 4), f[0], f[2]);
-              to_bf16<FMT>(word(lds16(sk + (KJ + k / 4) * 512), k % 4), f[1], f[3]);
+        tile_math<D, HM, true, true, TP>(
+            st, zf, vs, rows, lane,
+            [&](int u, int k, uint32_t (&f)[4]) {
+              to_f16<FMT>(word(kx[u][k / 4], k % 4), f[0], f[2]);
+              to_f16<FMT>(word(kx[u][KJ + k / 4], k % 4), f[1], f[3]);
             },
-            [&](int k, uint32_t (&f)[4]) {
-              uint32_t x[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                if constexpr (VP == 16) {
-                  x[i] = word(lds16(sv + i * 512), k / 2);
-                } else {
-                  const uint2 y = lds8(sv - lane * 8 + i * 256);
-                  x[i] = k / 2 == 0 ? y.x : y.y;
-                }
-              }
-              const uint32_t sel = k % 2 ? 0x7632 : 0x5410;
-              to_bf16<FMT>(__byte_perm(x[0], x[1], sel), f[0], f[1]);
-              to_bf16<FMT>(__byte_perm(x[2], x[3], sel), f[2], f[3]);
+            q_regs, v_load,
+            [&](int u, int k, uint32_t (&f)[4]) {
+              // the two tokens' bytes of column d, then of column d + 1
+              const uint32_t sel = k % 2 ? 0x7362 : 0x5140;
+              const int w = k / 2;
+              to_f16<FMT>(__byte_perm(word(vx[u][0], w), word(vx[u][1], w), sel), f[0], f[1]);
+              to_f16<FMT>(__byte_perm(word(vx[u][2], w), word(vx[u][3], w), sel), f[2], f[3]);
             });
       }
-    } else if (FMT != kBf16 && mt.page == -2) {
+    }
+    if (FMT != kBf16 && tail) {
       // the bf16 rows of the page that is not full, straight from memory, in
-      // the column orders of the 8-bit fragments
+      // the column orders of the 8-bit fragments; once for each listing
       const __nv_bfloat16* kt = a.k_tail + (size_t)bh * (kPage * D);
       const __nv_bfloat16* vt = a.v_tail + (size_t)bh * (kPage * D);
-      const int rows = mt.rows;
-      tile_math<D, NT>(
-          st, qb, a.scale_log2, 1.f, rows, lane,
-          [&](int k, uint32_t (&f)[4]) {
-            const int d = (t + 4 * (k / 4)) * 16 + (k % 4) * 4;
-            uint2 x = make_uint2(0, 0), y = make_uint2(0, 0);
-            if (g < rows) x = __ldg(reinterpret_cast<const uint2*>(kt + g * D + d));
-            if (g + 8 < rows) y = __ldg(reinterpret_cast<const uint2*>(kt + (g + 8) * D + d));
-            f[0] = __byte_perm(x.x, x.y, 0x5410);
-            f[1] = __byte_perm(y.x, y.y, 0x5410);
-            f[2] = __byte_perm(x.x, x.y, 0x7632);
-            f[3] = __byte_perm(y.x, y.y, 0x7632);
-          },
-          [&](int k, uint32_t (&f)[4]) {
-            const int d = g * (D / 8) + 2 * k;
-            uint32_t x[4];
+      float zt[1][NT][2];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int tok = 2 * t + (i & 1) + 8 * (i >> 1);
-              x[i] = tok < rows ? __ldg(reinterpret_cast<const uint32_t*>(vt + tok * D + d)) : 0u;
-            }
-            f[0] = __byte_perm(x[0], x[1], 0x5410);
-            f[1] = __byte_perm(x[0], x[1], 0x7632);
-            f[2] = __byte_perm(x[2], x[3], 0x5410);
-            f[3] = __byte_perm(x[2], x[3], 0x7632);
-          });
+      for (int nt = 0; nt < NT; ++nt) zt[0][nt][0] = zt[0][nt][1] = a.scale_log2;
+      const float one[1] = {1.f};
+      const int trows[1] = {tail_rows};
+      for (int u = 0; u < TP; ++u) {
+        if (meta[(i % S) * TP + u].page != -2) continue;
+        tile_math<D, HM, false, true, 1>(
+            st, zt, one, trows, lane,
+            [&](int, int k, uint32_t (&f)[4]) {
+              const int d = (t + 4 * (k / 4)) * 16 + (k % 4) * 4;
+              uint2 x = make_uint2(0, 0), y = make_uint2(0, 0);
+              if (g < tail_rows) x = __ldg(reinterpret_cast<const uint2*>(kt + g * D + d));
+              if (g + 8 < tail_rows) y = __ldg(reinterpret_cast<const uint2*>(kt + (g + 8) * D + d));
+              f[0] = x.x;
+              f[1] = y.x;
+              f[2] = x.y;
+              f[3] = y.y;
+            },
+            [&](int nt, int k, uint32_t& b0, uint32_t& b1) {
+              const uint2 x = q_at(nt, k);
+              b0 = x.x;
+              b1 = x.y;
+            },
+            []() {},
+            [&](int, int k, uint32_t (&f)[4]) {
+              const int d = g * (D / 8) + 2 * k;
+              uint32_t x[4];
+#pragma unroll
+              for (int r = 0; r < 4; ++r) {
+                const int tok = 2 * t + (r & 1) + 8 * (r >> 1);
+                x[r] = tok < tail_rows ? __ldg(reinterpret_cast<const uint32_t*>(vt + tok * D + d)) : 0u;
+              }
+              f[0] = __byte_perm(x[0], x[1], 0x5410);
+              f[1] = __byte_perm(x[0], x[1], 0x7632);
+              f[2] = __byte_perm(x[2], x[3], 0x5410);
+              f[3] = __byte_perm(x[2], x[3], 0x7632);
+            });
+      }
     }
   }
   cp_wait<0>();
@@ -457,7 +754,7 @@ __global__ void __launch_bounds__(Cfg<D, FMT, NT>::W * 32, Cfg<D, FMT, NT>::kCta
 #pragma unroll
       for (int j = 0; j < 2; ++j)
         *reinterpret_cast<float2*>(so + (size_t)(warp * NT * 8 + nt * 8 + 2 * t + j) * kLd + d) =
-            make_float2(st.o[nt][k][j], st.o[nt][k][j + 2]);
+            make_float2(st.o[nt][k][j] * st.vref, st.o[nt][k][j + 2] * st.vref);
     }
   if (g == 0) {
 #pragma unroll
@@ -468,21 +765,21 @@ __global__ void __launch_bounds__(Cfg<D, FMT, NT>::W * 32, Cfg<D, FMT, NT>::kCta
             make_float2(st.m[nt][j], st.l[nt][j]);
   }
   __syncthreads();
-  const int item = bh * a.n_chunks + blockIdx.x;
+  const bool whole = t0 == 0 && t1 == T;
+  const int item = blockIdx.x * 2 + (t0 > 0 ? 0 : 1);
   for (int e = threadIdx.x; e < a.G * D; e += W * 32) {
     const int n_ = e / D, d = e - n_ * D;
-    float M = -INFINITY;
+    float M = kNoMax;
 #pragma unroll
     for (int w = 0; w < W; ++w) M = fmaxf(M, sml[(w * NT * 8 + n_) * 2]);
-    const float ref = M == -INFINITY ? 0.f : M;
     float l = 0.f, o = 0.f;
 #pragma unroll
     for (int w = 0; w < W; ++w) {
-      const float f = fast_exp2(sml[(w * NT * 8 + n_) * 2] - ref);
+      const float f = fast_exp2(sml[(w * NT * 8 + n_) * 2] - M);
       l += f * sml[(w * NT * 8 + n_) * 2 + 1];
-      o += f * so[(size_t)(w * NT * 8 + n_) * kLd + d];
+      o += f * (so[(size_t)(w * NT * 8 + n_) * kLd + d] + (HM == kHalf ? so[(size_t)(w * 8 + n_ + 4) * kLd + d] : 0.f));
     }
-    if (a.n_chunks == 1) {
+    if (whole) {
       const size_t row = (size_t)b * a.Hq + h * a.G + n_;
       a.out[row * D + d] = l == 0.f ? 0.f : o / l;
       if (d == 0 && a.lse) a.lse[row] = l == 0.f ? -INFINITY : (M + fast_log2(l)) * kLn2;
@@ -493,27 +790,72 @@ __global__ void __launch_bounds__(Cfg<D, FMT, NT>::W * 32, Cfg<D, FMT, NT>::kCta
   }
 }
 
-// Merge of the chunks of one (sequence, query head): D threads per group of
-// chunks, four groups.
-template <int D>
-__global__ void __launch_bounds__(4 * D) page_merge_kernel(const __grid_constant__ PageAttnArgs a, int list) {
+template <int D, int FMT, int HM, bool LIST>
+__global__ void __launch_bounds__(Cfg<D, FMT, HM>::W * 32, Cfg<D, FMT, HM>::kCtas)
+    page_attn_kernel(const __grid_constant__ PageAttnArgs a) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   grid_dep_wait();
-  __shared__ float so[4][D], sl[4], sm[4];
+  grid_dep_launch();
+
+  // this CTA's run [pos, end) and the row it begins in
+  long long total, unused, pos, end, first;
+  int b;
+  count_tiles<LIST>(a, 0, lane, warp == 0 ? a.err : nullptr, total, unused);
+  pos = quota(total, a.ctas);
+  end = min(total, pos * (blockIdx.x + 1));
+  pos *= blockIdx.x;
+  if (pos >= end) return;
+  find_sequence<LIST>(a, pos, lane, b, first);
+
+  for (; pos < end; ++b) {   // sequences
+    const int len = seq_len(a.lens, a.L, b, nullptr);
+    const int blocks = (len + kPage - 1) / kPage;
+    const int T = LIST ? a.K : blocks;
+    if (T == 0) continue;
+    for (int h = (int)((pos - first) / T); h < a.Hkv && pos < end; ++h) {   // rows
+      const int t0 = (int)(pos - first - (long long)h * T);
+      const int t1 = (int)min((long long)T, t0 + (end - pos));
+      attend_row<D, FMT, HM, LIST>(a, smem, b, h, len, T, t0, t1);
+      pos += t1 - t0;
+      __syncthreads();   // the row's shared memory is free
+    }
+    first += (long long)T * a.Hkv;
+  }
+}
+// Merge of the pieces of a row for one query head: the CTAs whose runs the row
+// spans, D threads a piece, kGroups pieces at once.  Rows that one CTA finished
+// are passed over; rows without tiles get their empty result here.
+constexpr int kGroups = 4;
+template <int D, bool LIST>
+__global__ void __launch_bounds__(kGroups * D) page_merge_kernel(const __grid_constant__ PageAttnArgs a) {
+  grid_dep_wait();
+  __shared__ float so[kGroups][D], sl[kGroups], sm[kGroups];
   const int row = blockIdx.x, b = row / a.Hq, hq = row - b * a.Hq;
   const int h = hq / a.G, n_ = hq - h * a.G;
   const int grp = threadIdx.x / D, d = threadIdx.x % D;
-  const int len = seq_len(a.lens, a.L, b, nullptr);
-  const int T = list ? a.K : (len + kPage - 1) / kPage;
-  const int nc = (T + a.chunk - 1) / a.chunk;
-  const size_t first = (size_t)(b * a.Hkv + h) * a.n_chunks;
-  float M = -INFINITY, l = 0.f, o = 0.f;
-  for (int c = grp; c < nc; c += 4) {
-    const size_t r = (first + c) * a.G + n_;
+  long long total, first;
+  count_tiles<LIST>(a, b, threadIdx.x & 31, nullptr, total, first);
+  const int T = row_tiles<LIST>(a, b, nullptr);
+  if (T == 0) {
+    if (grp == 0) {
+      a.out[(size_t)row * D + d] = 0.f;
+      if (d == 0 && a.lse) a.lse[row] = -INFINITY;
+    }
+    return;
+  }
+  first += (long long)h * T;
+  const long long q = quota(total, a.ctas);
+  const int c0 = (int)(first / q), c1 = (int)((first + T - 1) / q);
+  if (c0 == c1) return;
+  float M = kNoMax, l = 0.f, o = 0.f;
+#pragma unroll 4
+  for (int c = c0 + grp; c <= c1; c += kGroups) {
+    const size_t r = ((size_t)c * 2 + (c > c0 ? 0 : 1)) * a.G + n_;   // only the first piece begins inside its run
     const float2 ml = __ldg(reinterpret_cast<const float2*>(a.ml + r * 2));
     const float x = __ldg(a.part + r * D + d);
     const float mn = fmaxf(M, ml.x);
-    const float ref = mn == -INFINITY ? 0.f : mn;
-    const float f0 = fast_exp2(M - ref), f1 = fast_exp2(ml.x - ref);
+    const float f0 = fast_exp2(M - mn), f1 = fast_exp2(ml.x - mn);
     l = l * f0 + ml.y * f1;
     o = o * f0 + x * f1;
     M = mn;
@@ -525,12 +867,13 @@ __global__ void __launch_bounds__(4 * D) page_merge_kernel(const __grid_constant
   }
   __syncthreads();
   if (grp != 0) return;
-  M = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
-  const float ref = M == -INFINITY ? 0.f : M;
+  M = kNoMax;
+#pragma unroll
+  for (int i = 0; i < kGroups; ++i) M = fmaxf(M, sm[i]);
   l = o = 0.f;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float f = fast_exp2(sm[i] - ref);
+  for (int i = 0; i < kGroups; ++i) {
+    const float f = fast_exp2(sm[i] - M);
     l += f * sl[i];
     o += f * so[i][d];
   }
@@ -550,24 +893,35 @@ sfi_status cuda_status(cudaError_t e) {
   return SFI_ERR_CUDA;
 }
 
-template <int D, int FMT, int NT, bool LIST>
-sfi_status launch(const PageAttnArgs& a, cudaStream_t st) {
-  using C = Cfg<D, FMT, NT>;
-  auto k = page_attn_kernel<D, FMT, NT, LIST>;
+template <int D, int FMT, int HM, bool LIST>
+sfi_status launch(PageAttnArgs& a, cudaStream_t st) {
+  using C = Cfg<D, FMT, HM>;
+  auto k = page_attn_kernel<D, FMT, HM, LIST>;
   static DeviceOnce once;
   if (!once.done()) {
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (!once.mark(e)) return cuda_status(e);
   }
-  const sfi_status r = cuda_status(launch_k(k, dim3(a.n_chunks, a.B * a.Hkv), dim3(C::W * 32), C::kSmem, st, a));
-  if (r != SFI_OK || a.n_chunks == 1) return r;
-  return cuda_status(launch_k(page_merge_kernel<D>, dim3(a.B * a.Hq), dim3(4 * D), 0, st, a, LIST ? 1 : 0));
+  const int T = LIST ? a.K : (a.L + kPage - 1) / kPage;
+  const long long total = (long long)a.B * a.Hkv * T;
+  a.ctas = page_attn_ctas(total, C::kCtas);
+  const sfi_status r = cuda_status(launch_k(k, dim3(a.ctas), dim3(C::W * 32), C::kSmem, st, a));
+  // no row is cut when every run is a whole number of rows of one length
+  const bool cut = (!LIST && a.lens) || quota(total, a.ctas) % T != 0;
+  if (r != SFI_OK || !cut) return r;
+  return cuda_status(launch_k(page_merge_kernel<D, LIST>, dim3(a.B * a.Hq), dim3(kGroups * D), 0, st, a));
+}
+
+template <int D, int FMT, bool LIST>
+sfi_status launch_heads(PageAttnArgs& a, cudaStream_t st) {
+  if (a.G > 8) return launch<D, FMT, kTwo, LIST>(a, st);
+  if (a.G > 4) return launch<D, FMT, kOne, LIST>(a, st);
+  return launch<D, FMT, kHalf, LIST>(a, st);
 }
 
 template <int FMT, bool LIST>
-sfi_status launch_any(int D, const PageAttnArgs& a, cudaStream_t st) {
-  if (D == 128) return a.G > 8 ? launch<128, FMT, 2, LIST>(a, st) : launch<128, FMT, 1, LIST>(a, st);
-  return a.G > 8 ? launch<64, FMT, 2, LIST>(a, st) : launch<64, FMT, 1, LIST>(a, st);
+sfi_status launch_any(int D, PageAttnArgs& a, cudaStream_t st) {
+  return D == 128 ? launch_heads<128, FMT, LIST>(a, st) : launch_heads<64, FMT, LIST>(a, st);
 }
 
 // Shared by the three entry points: kv (bf16) or q8 (8-bit) is the cache.
@@ -587,7 +941,6 @@ sfi_status run(const sfi_shape* shape, const sfi_paged_kv* kv, const sfi_quant_k
   if (BHl > 65535) return SFI_ERR_UNSUPPORTED;
   const BlockWs w = block_ws(*shape);
   if (!ws || !aligned16(ws) || ws_bytes < w.total) return SFI_ERR_WORKSPACE;
-  const int BH = (int)BHl;
   PageAttnArgs a{};
   a.B = shape->B;
   a.Hq = shape->Hq;
@@ -616,10 +969,6 @@ sfi_status run(const sfi_shape* shape, const sfi_paged_kv* kv, const sfi_quant_k
   a.sel = sel;
   a.sel_ld = sel_ld;
   a.K = K;
-  const int T = list ? K : (L + kPage - 1) / kPage;
-  const int nc = page_attn_chunks(BH, a.G, T);
-  a.chunk = (T + nc - 1) / nc;
-  a.n_chunks = (T + a.chunk - 1) / a.chunk;
   a.scale_log2 = kLog2e / sqrtf((float)shape->D);
   a.out = out;
   a.lse = lse;
@@ -635,13 +984,11 @@ sfi_status run(const sfi_shape* shape, const sfi_paged_kv* kv, const sfi_quant_k
 
 }  // namespace
 
-// Chunks of a (sequence, KV head) with T tiles: about four waves of two CTAs
-// per SM, at least 16 tiles a chunk.
-int page_attn_chunks(int BH, int G, int T) {
-  const int want = std::max(1, num_sms() * 8 / BH);
-  return std::max(1, std::min(want, (T + 15) / 16));
+// One wave of `per_sm` CTAs a multiprocessor, fewer where the tiles would not
+// give each kMinQuota.
+int page_attn_ctas(long long tiles, int per_sm) {
+  return (int)std::max(1LL, std::min((long long)num_sms() * per_sm, (tiles + kMinQuota - 1) / kMinQuota));
 }
-int page_attn_chunks_bound(int BH, int G, int Tmax) { return page_attn_chunks(BH, G, Tmax); }
 
 }  // namespace sfi
 

@@ -7,7 +7,11 @@ rounded to bf16 twice (hi + lo), 2^-8 * 2^-8 of itself; a logit is off by at mos
 (D / 16 + 2) * 2^-23 * sum |q k| / sqrt(D) (one fp32 rounding, truncation
 allowed for, per matrix step) plus 2^-22 of itself for the scaling, which moves
 P by twice that; the sums over tokens and warps add at most (tiles + 64) * 2^-23.
-All of it relative to sum p |v|.
+All of it relative to sum p |v|.  On the 8-bit cache P is fp16 (rounded twice, less
+than the bf16 term above), where besides a value below fp16's smallest step is lost:
+that step is 2^-24, P's largest value at least 2^8 and the sum of P at least that, so a
+weight P / sum P is off by at most half a step over 2^8, 2^-33, and an output by at most
+2^-33 sum |v| more.
 """
 import math
 
@@ -103,7 +107,8 @@ def check_attn(got, lse, q, K, V, what):
         return
     dz = (D / 16 + 2) * 2.0 ** -23 * s + 2.0 ** -22 * np.abs(s)
     rel = 2.0 ** -16 + 2 * dz + (len(K) / 16 + 64) * 2.0 ** -23
-    assert np.all(np.abs(got - o) <= rel[:, None] * pv + 1e-30), (what, np.abs(got - o).max(), (rel[:, None] * pv).min())
+    tol = rel[:, None] * pv + 2.0 ** -33 * np.abs(V).sum(0) + 1e-30
+    assert np.all(np.abs(got - o) <= tol), (what, (np.abs(got - o) / tol).max())
     assert np.all(np.abs(lse - ref_lse) <= 2 * dz + (len(K) / 16 + 64) * 2.0 ** -23 + 2.0 ** -22 * np.abs(ref_lse)), what
 
 
@@ -276,7 +281,9 @@ def test_quant_attention(fmt, B, Hq, Hkv, D, lens):
 
 @pytest.mark.parametrize("fmt", FMTS)
 def test_every_code_is_read_exactly(fmt):
-    """V rows hold every code; one token holds all the weight, so the output is the code's value."""
+    """V rows hold every code; one token holds all the weight, so the output is the code's value,
+    but for P's two fp16 roundings (2^-11 * 2^-11 of it) and four fp32 ones: less than 2^-21, and
+    neighbouring codes are 2^-7 or more apart."""
     c = Case(1, 1, 1, 128, [64], fmt, seed=6).up()
     S.sfi_quant_store(c.shape, c.kv, c.q8, 0, 64)
     vals = [x for x in range(256) if not (fmt == "e4m3" and (x & 127) == 127)]
@@ -295,7 +302,7 @@ def test_every_code_is_read_exactly(fmt):
         S.sfi_quant_attn(c.shape, c.q8, 64, c.qd, c.out, c.ws)
         assert c.error() == 0
         want = P.code_values(codes[row].numpy(), fmt) * 0.5
-        assert np.array_equal(c.out.cpu().double().numpy()[0, 0], want)
+        assert np.all(np.abs(c.out.cpu().double().numpy()[0, 0] - want) <= 2.0 ** -21 * np.abs(want))
 
 
 @pytest.mark.parametrize("fmt", FMTS)
