@@ -12,11 +12,12 @@
 // each warp runs its own online softmax and the CTA merges its warps in shared
 // memory.
 //
-// Bound by reading the cache, so the layout serves the loads.  Every warp
-// streams its tiles through its own ring of stages with 16-byte asynchronous
-// copies, and each thread copies exactly the bytes its own matrix fragments
-// need: no barrier, no swizzle, no bank conflict, and no wait that another
-// warp has to end.  That works because the order of a contraction is free:
+// Bound by reading the cache, so the layout serves the loads.  Each thread loads
+// exactly the bytes its own matrix fragments need, 16 at a time, straight into
+// registers: the next tile's K while the softmax and V^T P^T of this one run,
+// its V while the next S^T does.  No shared memory, no barrier and no wait that
+// another warp has to end.  That works because the order of a contraction is
+// free:
 //   S^T[16 tok x 8 heads] = K[16 x D] . Q^T[D x 8]: thread (g, t) of the
 //     fragment layout (g = lane / 4, t = lane % 4) holds rows g, g + 8 and any
 //     D / 4 of the columns, as long as Q is laid out alike: the 16-byte chunks
@@ -73,17 +74,23 @@ struct PageAttnArgs {
 // HM, how the group's heads fill the 8 columns of a product: kHalf (G <= 4) has
 // heads 0 .. 3 twice, the second time with the low part of P, so one product
 // serves both parts; kOne (G <= 8) and kTwo (G <= 16) take hi and lo in turn.
-#ifndef PA_TP
-#define PA_TP 2
-#endif
 #ifndef PA_W
-#define PA_W 6
+#define PA_W 8
 #endif
-#ifndef PA_S
-#define PA_S 2
+#ifndef PA_WB
+#define PA_WB 6
+#endif
+#ifndef PA_W2
+#define PA_W2 4
+#endif
+#ifndef PA_CT
+#define PA_CT 2
 #endif
 #ifndef PA_MINQ
-#define PA_MINQ 12
+#define PA_MINQ 16
+#endif
+#ifndef PA_WAVES
+#define PA_WAVES 1
 #endif
 enum HeadMap : int { kHalf = 0, kOne = 1, kTwo = 2 };
 
@@ -92,22 +99,14 @@ struct Cfg {
   static constexpr int NT = HM == kTwo ? 2 : 1;         // column tiles
   static constexpr int kEl = FMT == kBf16 ? 2 : 1;
   static constexpr int kRow = D * kEl;                  // bytes of a row
-  static constexpr int KJ = kRow / 64;                  // 16-byte chunks of a K row per thread
+  static constexpr int KJ = kRow / 64;                  // 16-byte pieces of a K row per thread
   static constexpr int kVB = kRow / 8;                  // bytes of a V row per thread: 8, 16 or 32
   static constexpr int VC = kVB >= 16 ? kVB / 16 : 1;   // pieces of them
   static constexpr int VP = kVB >= 16 ? 16 : 8;         // bytes of a piece
-  static constexpr int kKBytes = 16 * kRow;             // of a tile, K and V alike
-  static constexpr int kTile = 2 * kKBytes;
-  // A step is TP tiles, a stage holds one step.
-  static constexpr int TP = FMT == kBf16 ? 1 : PA_TP;
-  static constexpr int W = FMT == kBf16 ? 4 : PA_W;
-  static constexpr int kCtas = NT == 1 ? 2 : 1;
-  static constexpr int kStage = TP * kTile;
-  static constexpr int S = FMT == kBf16 ? 3 : PA_S;
-  static constexpr int kRing = W * S * kStage;
-  static constexpr int kMerge = W * NT * 8 * (D + 8) * 4 + W * NT * 8 * 2 * 4;
-  static constexpr int kMeta = W * S * TP * 16;
-  static constexpr int kSmem = (kRing > kMerge ? kRing : kMerge) + kMeta;
+  static constexpr int kTile = 16 * kRow;               // bytes of a tile of K, and of V
+  static constexpr int W = NT == 2 ? PA_W2 : FMT == kBf16 ? PA_WB : PA_W;   // warps
+  static constexpr int kCtas = NT == 2 ? 2 : PA_CT;                   // per SM
+  static constexpr int kSmem = W * NT * 8 * (D + 8) * 4 + W * NT * 8 * 2 * 4;   // merge of the warps
 };
 
 // The run of each CTA is `quota` tiles of the whole sequence.
@@ -182,28 +181,26 @@ __device__ __forceinline__ void find_sequence(const PageAttnArgs& a, long long p
   first = base;
 }
 
-struct Meta {       // of a stage
+struct Tile {
   int page;         // >= 0; -1: nothing; -2: the tail
   int rows;         // valid rows
   float ks, vs;
 };
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+// 16 or 8 bytes of the cache, read once: kept in program order, so that a load
+// stays where the code issues it, ahead of the work it overlaps.
+__device__ __forceinline__ uint4 ld16(const uint8_t* p) {
+  uint4 r;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p));
+  return r;
 }
-__device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, int bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+__device__ __forceinline__ uint4 ld8(const uint8_t* p) {
+  uint4 r = make_uint4(0, 0, 0, 0);
+  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
+  return r;
 }
-__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ uint4 lds16(const uint8_t* p) { return *reinterpret_cast<const uint4*>(p); }
-__device__ __forceinline__ uint2 lds8(const uint8_t* p) { return *reinterpret_cast<const uint2*>(p); }
 
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   const __half2 v = __floats2half2_rn(lo, hi);
@@ -283,48 +280,40 @@ __device__ __forceinline__ void scale_o(State<D, NT>& st, float f) {
       for (int i = 0; i < 4; ++i) st.o[nt][k][i] *= f;
 }
 
-// TP tiles from their fragments: kf(tile, step, a) and vf(tile, step, a) fill
-// the A operands of S^T and O^T, qf(column tile, step, b0, b1) the B operand of
-// S^T; vload() runs between the two products.  zf: log2 units per unit of S^T,
-// per tile and head; vs: the value scales; rows: valid rows (0: no tile).
-// F16: fp16 operands (8-bit pages), else bf16.  SCALED: the cache has value
-// scales.
-template <int D, int HM, bool F16, bool SCALED, int TP, class KF, class QF, class VL, class VF, int NT>
-__device__ __forceinline__ void tile_math(State<D, NT>& st, const float (&zf)[TP][NT][2], const float (&vs)[TP],
-                                          const int (&rows)[TP], int lane, KF kf, QF qf, VL vload, VF vf) {
-  float s[TP][NT][4], x[TP][NT][4];
+// One tile from its fragments: kf(step, a) and vf(step, a) fill the A operands
+// of S^T and O^T, qf(column tile, step, b0, b1) the B operand of S^T; between()
+// runs once K is used up.  zf: log2 units per unit of S^T, per head; vs: the
+// value scale; rows: valid rows.  F16: fp16 operands (8-bit pages), else bf16.
+// SCALED: the cache has value scales.
+template <int D, int HM, bool F16, bool SCALED, class KF, class QF, class BW, class VF, int NT>
+__device__ __forceinline__ void tile_math(State<D, NT>& st, const float (&zf)[NT][2], float vs, int rows, int lane,
+                                          KF kf, QF qf, BW between, VF vf) {
+  float s[NT][4], x[NT][4];
 #pragma unroll
   for (int k = 0; k < D / 16; ++k) {
-    uint32_t a[TP][4];
-#pragma unroll
-    for (int u = 0; u < TP; ++u) kf(u, k, a[u]);
+    uint32_t a[4];
+    kf(k, a);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       uint32_t b0, b1;
       qf(nt, k, b0, b1);
-#pragma unroll
-      for (int u = 0; u < TP; ++u) {
-        if (k == 0) mma16<F16, false>(s[u][nt], a[u], b0, b1);
-        else if (k == 1) mma16<F16, false>(x[u][nt], a[u], b0, b1);
-        else if (k % 2 == 0) mma16<F16, true>(s[u][nt], a[u], b0, b1);
-        else mma16<F16, true>(x[u][nt], a[u], b0, b1);
-      }
+      if (k == 0) mma16<F16, false>(s[nt], a, b0, b1);
+      else if (k == 1) mma16<F16, false>(x[nt], a, b0, b1);
+      else if (k % 2 == 0) mma16<F16, true>(s[nt], a, b0, b1);
+      else mma16<F16, true>(x[nt], a, b0, b1);
     }
   }
-  vload();
+  between();
   bool grow = false;
 #pragma unroll
-  for (int u = 0; u < TP; ++u)
+  for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        s[u][nt][i] += x[u][nt][i];
-        // one rounding, of the difference; no tile: s is 0
-        x[u][nt][i] = fmaf(s[u][nt][i], zf[u][nt][i & 1], TP > 1 && rows[u] == 0 ? -INFINITY : -st.m[nt][i & 1]);
-        if (TP == 1 && rows[u] < kPage && (lane >> 2) + 8 * (i >> 1) >= rows[u]) x[u][nt][i] = -INFINITY;
-        grow |= x[u][nt][i] > kBias + kSlack;
-      }
+    for (int i = 0; i < 4; ++i) {
+      s[nt][i] += x[nt][i];
+      x[nt][i] = fmaf(s[nt][i], zf[nt][i & 1], -st.m[nt][i & 1]);   // one rounding, of the difference
+      if (!F16 && rows < kPage && (lane >> 2) + 8 * (i >> 1) >= rows) x[nt][i] = -INFINITY;   // 8-bit pages are full
+      grow |= x[nt][i] > kBias + kSlack;
+    }
   if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -332,10 +321,8 @@ __device__ __forceinline__ void tile_math(State<D, NT>& st, const float (&zf)[TP
       for (int j = 0; j < 2; ++j) {
         float z = -INFINITY;
 #pragma unroll
-        for (int u = 0; u < TP; ++u)
-#pragma unroll
-          for (int r = 0; r < 2; ++r)
-            if (x[u][nt][j + 2 * r] != -INFINITY) z = fmaxf(z, s[u][nt][j + 2 * r] * zf[u][nt][j]);
+        for (int r = 0; r < 2; ++r)
+          if (x[nt][j + 2 * r] != -INFINITY) z = fmaxf(z, s[nt][j + 2 * r] * zf[nt][j]);
 #pragma unroll
         for (int sh = 4; sh <= 16; sh <<= 1) z = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, sh));
         const float mn = fmaxf(st.m[nt][j], z - kBias);
@@ -348,90 +335,74 @@ __device__ __forceinline__ void tile_math(State<D, NT>& st, const float (&zf)[TP
           st.o[nt][k][j + 2] *= al;
         }
 #pragma unroll
-        for (int u = 0; u < TP; ++u)
-#pragma unroll
-          for (int r = 0; r < 2; ++r)
-            if (x[u][nt][j + 2 * r] != -INFINITY)
-              x[u][nt][j + 2 * r] = fmaf(s[u][nt][j + 2 * r], zf[u][nt][j], -mn);
+        for (int r = 0; r < 2; ++r)
+          if (x[nt][j + 2 * r] != -INFINITY) x[nt][j + 2 * r] = fmaf(s[nt][j + 2 * r], zf[nt][j], -mn);
       }
   }
   // The value scale multiplies P, relative to vref so that fp16 holds it: vref
   // follows the largest scale seen (within a factor of 2); a page whose scale
   // is 2^6 and more below it, which fp16 would hold less exactly, has its
   // product scaled instead.
-  float pv[TP];
+  float pv = 1.f;
   bool apart = false;
-#pragma unroll
-  for (int u = 0; u < TP; ++u) pv[u] = 1.f;
   if constexpr (SCALED) {
-#pragma unroll
-    for (int u = 0; u < TP; ++u)
-      if (!(vs[u] <= 2.f * st.vref)) {   // NaN too
-        scale_o(st, __fdiv_rn(st.vref, vs[u]));
-        st.vref = vs[u];
-        st.vinv = __fdiv_rn(1.f, vs[u]);
-      }
-#pragma unroll
-    for (int u = 0; u < TP; ++u) {
-      pv[u] = vs[u] * st.vinv;
-      apart |= F16 && pv[u] < 0.015625f && rows[u] > 0;
+    if (!(vs <= 2.f * st.vref)) {   // NaN too
+      scale_o(st, __fdiv_rn(st.vref, vs));
+      st.vref = vs;
+      st.vinv = __fdiv_rn(1.f, vs);
     }
+    pv = vs * st.vinv;
+    // the same in every lane; the vote lets the compiler branch
+    if (F16) apart = __any_sync(0xffffffffu, pv < 0.015625f);
   }
-  apart = SCALED && F16 && __any_sync(0xffffffffu, apart);   // the same in every lane; a vote lets the compiler branch
-  uint32_t hi[TP][NT][2], lo[TP][NT][2];
+  uint32_t hi[NT][2], lo[NT][2];
 #pragma unroll
-  for (int u = 0; u < TP; ++u)
+  for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        float p0 = fast_exp2(x[u][nt][2 * r]), p1 = fast_exp2(x[u][nt][2 * r + 1]);
-        st.l[nt][0] += p0;
-        st.l[nt][1] += p1;
-        if constexpr (SCALED) {
-          const float f = apart ? 1.f : pv[u];
-          p0 *= f;
-          p1 *= f;
-        }
-        const uint32_t h = F16 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
-        const float2 f = F16 ? unpack_f16x2(h) : unpack_bf16x2(h);
-        const uint32_t q = F16 ? pack_f16x2(p0 - f.x, p1 - f.y) : pack_bf16x2(p0 - f.x, p1 - f.y);
-        if constexpr (HM == kHalf) {
-          hi[u][nt][r] = movmatrix_trans((lane & 2) ? q : h);
-        } else {
-          hi[u][nt][r] = movmatrix_trans(h);
-          lo[u][nt][r] = movmatrix_trans(q);
-        }
+    for (int r = 0; r < 2; ++r) {
+      float p0 = fast_exp2(x[nt][2 * r]), p1 = fast_exp2(x[nt][2 * r + 1]);
+      st.l[nt][0] += p0;
+      st.l[nt][1] += p1;
+      if constexpr (SCALED) {
+        const float f = apart ? 1.f : pv;
+        p0 *= f;
+        p1 *= f;
       }
+      const uint32_t h = F16 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
+      const float2 f = F16 ? unpack_f16x2(h) : unpack_bf16x2(h);
+      const uint32_t q = F16 ? pack_f16x2(p0 - f.x, p1 - f.y) : pack_bf16x2(p0 - f.x, p1 - f.y);
+      if constexpr (HM == kHalf) {
+        hi[nt][r] = movmatrix_trans((lane & 2) ? q : h);
+      } else {
+        hi[nt][r] = movmatrix_trans(h);
+        lo[nt][r] = movmatrix_trans(q);
+      }
+    }
   if (SCALED && F16 && apart) {
 #pragma unroll
-    for (int k = 0; k < D / 16; ++k)
+    for (int k = 0; k < D / 16; ++k) {
+      uint32_t a[4];
+      vf(k, a);
 #pragma unroll
-      for (int u = 0; u < TP; ++u) {
-        uint32_t a[4];
-        vf(u, k, a);
+      for (int nt = 0; nt < NT; ++nt) {
+        float c[4];
+        mma16<F16, false>(c, a, hi[nt][0], hi[nt][1]);
+        if constexpr (HM != kHalf) mma16<F16, true>(c, a, lo[nt][0], lo[nt][1]);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float c[4];
-          mma16<F16, false>(c, a, hi[u][nt][0], hi[u][nt][1]);
-          if constexpr (HM != kHalf) mma16<F16, true>(c, a, lo[u][nt][0], lo[u][nt][1]);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) st.o[nt][k][i] = fmaf(pv[u], c[i], st.o[nt][k][i]);
-        }
+        for (int i = 0; i < 4; ++i) st.o[nt][k][i] = fmaf(pv, c[i], st.o[nt][k][i]);
       }
+    }
   } else {
 #pragma unroll
-    for (int k = 0; k < D / 16; ++k)
+    for (int k = 0; k < D / 16; ++k) {
+      uint32_t a[4];
+      vf(k, a);
 #pragma unroll
-      for (int u = 0; u < TP; ++u) {
-        uint32_t a[4];
-        vf(u, k, a);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          mma16<F16, true>(st.o[nt][k], a, hi[u][nt][0], hi[u][nt][1]);
-          if constexpr (HM != kHalf) mma16<F16, true>(st.o[nt][k], a, lo[u][nt][0], lo[u][nt][1]);
-        }
+      for (int nt = 0; nt < NT; ++nt) {
+        mma16<F16, true>(st.o[nt][k], a, hi[nt][0], hi[nt][1]);
+        if constexpr (HM != kHalf) mma16<F16, true>(st.o[nt][k], a, lo[nt][0], lo[nt][1]);
       }
+    }
   }
 }
 
@@ -441,7 +412,7 @@ template <int D, int FMT, int HM, bool LIST>
 __device__ __forceinline__ void attend_row(const PageAttnArgs& a, uint8_t* smem, int b, int h, int len, int T, int t0,
                                            int t1) {
   using C = Cfg<D, FMT, HM>;
-  constexpr int NT = C::NT, TP = C::TP, W = C::W, S = C::S, KJ = C::KJ, VC = C::VC, VP = C::VP;
+  constexpr int NT = C::NT, W = C::W, KJ = C::KJ, VC = C::VC, VP = C::VP;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const int bh = b * a.Hkv + h;
@@ -490,17 +461,12 @@ __device__ __forceinline__ void attend_row(const PageAttnArgs& a, uint8_t* smem,
     }
   }
 
-  uint8_t* ring = smem + (size_t)warp * S * C::kStage;
-  const uint32_t ring_u = smem_u32(ring) + lane * 16;
-  Meta* meta = reinterpret_cast<Meta*>(smem + (C::kSmem - C::kMeta)) + warp * S * TP;
-
-  // Tiles of this warp: t0 + warp + W * i, i < n, in steps of TP.  Lane l looks
-  // up tile i0 + l of a batch of 32: block, page and scales.
+  // Tiles of this warp: t0 + warp + W * i, i < n.  Lane l looks up tile i0 + l of
+  // a batch of 32: block, page and scales.
   const int n = t1 - t0 > warp ? (t1 - t0 - warp + W - 1) / W : 0;
-  const int steps = (n + TP - 1) / TP;
-  Meta mine{-1, 0, 0.f, 0.f};
+  Tile mine{-1, 0, 0.f, 0.f};
   auto look_up = [&](int i0) {
-    mine = Meta{-1, 0, 0.f, 0.f};
+    mine = Tile{-1, 0, 0.f, 0.f};
     const int i = i0 + lane;
     if (i >= n) return;
     const int tile = t0 + warp + W * i;
@@ -524,59 +490,41 @@ __device__ __forceinline__ void attend_row(const PageAttnArgs& a, uint8_t* smem,
     }
   };
 
-  // copies of step i into stage i % S
-  auto issue = [&](int i) {
-    if (i < steps) {
-      const int first = i * TP;
-      if ((first & 31) == 0) look_up(first);
-      const int st = i % S;
-      if (lane - (first & 31) >= 0 && lane - (first & 31) < TP) meta[st * TP + lane - (first & 31)] = mine;
+  auto tile_at = [&](int i) {
+    Tile x{-1, 0, 0.f, 0.f};
+    if (i >= n) return x;
+    if ((i & 31) == 0) look_up(i);
+    x.page = __shfl_sync(0xffffffffu, mine.page, i & 31);
+    x.rows = __shfl_sync(0xffffffffu, mine.rows, i & 31);
+    if (FMT != kBf16) {
+      x.ks = __shfl_sync(0xffffffffu, mine.ks, i & 31);
+      x.vs = __shfl_sync(0xffffffffu, mine.vs, i & 31);
+    }
+    return x;
+  };
+  uint4 kx[2 * KJ], vx[4 * VC];
+  const uint8_t* k0 = a.k + (size_t)h * C::kTile + g * C::kRow + t * 16;
+  const uint8_t* v0 = a.v + (size_t)h * C::kTile + 2 * t * C::kRow + g * VP;
+  auto load_k = [&](const Tile& x) {
+    const uint8_t* p = k0 + (size_t)x.page * a.Hkv * C::kTile;
 #pragma unroll
-      for (int u = 0; u < TP; ++u) {
-        const int src = (first + u) & 31;
-        const int page = __shfl_sync(0xffffffffu, mine.page, src);
-        if (page < 0) {
-          // no tile in this place of the step: zeros, which its mask then drops
-          if (TP > 1)
+    for (int r = 0; r < 2; ++r)
 #pragma unroll
-            for (int x = 0; x < C::kTile / 512; ++x)
-              *reinterpret_cast<uint4*>(ring + st * C::kStage + u * C::kTile + x * 512 + lane * 16) = make_uint4(0, 0, 0, 0);
-          continue;
-        }
-        const size_t off = ((size_t)page * a.Hkv + h) * C::kKBytes;
-        const uint8_t* kp = a.k + off + g * C::kRow + t * 16;
-        const uint8_t* vp = a.v + off + 2 * t * C::kRow + g * VP;
-        const uint32_t sk = ring_u + st * C::kStage + u * C::kTile, sv = sk + C::kKBytes;
-        if constexpr (FMT == kBf16) {
-          const int rows = __shfl_sync(0xffffffffu, mine.rows, src);
+      for (int j = 0; j < KJ; ++j)
+        kx[r * KJ + j] = FMT != kBf16 || g + 8 * r < x.rows ? ld16(p + r * 8 * C::kRow + j * 64) : make_uint4(0, 0, 0, 0);
+  };
+  auto load_v = [&](const Tile& x) {
+    const uint8_t* p = v0 + (size_t)x.page * a.Hkv * C::kTile;
 #pragma unroll
-          for (int r = 0; r < 2; ++r)
+    for (int i = 0; i < 4; ++i) {
+      const int tok = (i & 1) + 8 * (i >> 1);
 #pragma unroll
-            for (int j = 0; j < KJ; ++j)
-              cp_async16_zfill(sk + (r * KJ + j) * 512, kp + r * 8 * C::kRow + j * 64, g + 8 * r < rows ? 16 : 0);
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const int tok = (x & 1) + 8 * (x >> 1);
-#pragma unroll
-            for (int c = 0; c < VC; ++c)
-              cp_async16_zfill(sv + (x * VC + c) * 512, vp + tok * C::kRow + c * 128, 2 * t + tok < rows ? 16 : 0);
-          }
-        } else {
-#pragma unroll
-          for (int r = 0; r < 2; ++r)
-#pragma unroll
-            for (int j = 0; j < KJ; ++j)
-              cp_async16(sk + (r * KJ + j) * 512, kp + r * 8 * C::kRow + j * 64);
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const int tok = (x & 1) + 8 * (x >> 1);
-            if constexpr (VP == 16) cp_async16(sv + x * 512, vp + tok * C::kRow);
-            else cp_async8(sv - lane * 8 + x * 256, vp + tok * C::kRow);
-          }
-        }
+      for (int c = 0; c < VC; ++c) {
+        const uint8_t* at = p + tok * C::kRow + c * 128;
+        if constexpr (VP == 8) vx[i] = ld8(at);
+        else vx[i * VC + c] = FMT != kBf16 || 2 * t + tok < x.rows ? ld16(at) : make_uint4(0, 0, 0, 0);
       }
     }
-    cp_commit();
   };
 
   State<D, NT> st;
@@ -595,110 +543,77 @@ __device__ __forceinline__ void attend_row(const PageAttnArgs& a, uint8_t* smem,
       for (int i = 0; i < 4; ++i) st.o[nt][k][i] = 0.f;
   }
 
-#pragma unroll
-  for (int i = 0; i < S - 1; ++i) issue(i);
   auto q_regs = [&](int nt, int k, uint32_t& b0, uint32_t& b1) {
     b0 = qb[nt][k][0];
     b1 = qb[nt][k][1];
   };
-  for (int i = 0; i < steps; ++i) {
-    __syncwarp();   // every lane has read stage (i - 1) % S's description
-    issue(i + S - 1);
-    cp_wait<S - 1>();
-    __syncwarp();
-    const uint8_t* sk = ring + (i % S) * C::kStage + lane * 16;
-    float zf[TP][NT][2], vs[TP];
-    int rows[TP];
-    bool any = false, tail = false;
-    int tail_rows = 0;
-#pragma unroll
-    for (int u = 0; u < TP; ++u) {
-      const Meta mt = meta[(i % S) * TP + u];
-      rows[u] = mt.page >= 0 ? mt.rows : 0;
-      any |= mt.page >= 0;
-      if (mt.page == -2) {
-        tail = true;
-        tail_rows = mt.rows;
-      }
-      vs[u] = mt.vs;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) zf[u][nt][j] = FMT == kBf16 ? a.scale_log2 : zq[nt][j] * mt.ks;
-    }
-    if (any) {
-      uint4 kx[TP][2 * KJ], vx[TP][4 * VC];
-#pragma unroll
-      for (int u = 0; u < TP; ++u)
-#pragma unroll
-        for (int j = 0; j < 2 * KJ; ++j) kx[u][j] = lds16(sk + u * C::kTile + j * 512);
-      auto v_load = [&]() {
-#pragma unroll
-        for (int u = 0; u < TP; ++u) {
-          const uint8_t* sv = sk + u * C::kTile + C::kKBytes;
-#pragma unroll
-          for (int x = 0; x < 4 * VC; ++x) {
-            if constexpr (VP == 16) {
-              vx[u][x] = lds16(sv + x * 512);
-            } else {
-              const uint2 y = lds8(sv - lane * 8 + x * 256);
-              vx[u][x] = make_uint4(y.x, y.y, 0, 0);
-            }
-          }
-        }
-      };
+  Tile cur = tile_at(0);
+  if (cur.page >= 0) {
+    load_k(cur);
+    load_v(cur);
+  }
+  for (int i = 0; i < n; ++i) {
+    const Tile nxt = tile_at(i + 1);
+    auto next_k = [&]() {
+      if (nxt.page >= 0) load_k(nxt);
+    };
+    if (cur.page >= 0) {
       if constexpr (FMT == kBf16) {
-        tile_math<D, HM, false, false, TP>(
-            st, zf, vs, rows, lane,
-            [&](int u, int k, uint32_t (&f)[4]) {
+        tile_math<D, HM, false, false>(
+            st, zq, 1.f, cur.rows, lane,
+            [&](int k, uint32_t (&f)[4]) {
               const int w = (k % 2) * 2;
-              f[0] = word(kx[u][k / 2], w);
-              f[1] = word(kx[u][KJ + k / 2], w);
-              f[2] = word(kx[u][k / 2], w + 1);
-              f[3] = word(kx[u][KJ + k / 2], w + 1);
+              f[0] = word(kx[k / 2], w);
+              f[1] = word(kx[KJ + k / 2], w);
+              f[2] = word(kx[k / 2], w + 1);
+              f[3] = word(kx[KJ + k / 2], w + 1);
             },
-            q_regs, v_load,
-            [&](int u, int k, uint32_t (&f)[4]) {
+            q_regs, next_k,
+            [&](int k, uint32_t (&f)[4]) {
               const int c = k / 4, w = k % 4;
-              const uint32_t x0 = word(vx[u][c], w), x1 = word(vx[u][VC + c], w);
-              const uint32_t x2 = word(vx[u][2 * VC + c], w), x3 = word(vx[u][3 * VC + c], w);
+              const uint32_t x0 = word(vx[c], w), x1 = word(vx[VC + c], w);
+              const uint32_t x2 = word(vx[2 * VC + c], w), x3 = word(vx[3 * VC + c], w);
               f[0] = __byte_perm(x0, x1, 0x5410);
               f[1] = __byte_perm(x0, x1, 0x7632);
               f[2] = __byte_perm(x2, x3, 0x5410);
               f[3] = __byte_perm(x2, x3, 0x7632);
             });
       } else {
-        tile_math<D, HM, true, true, TP>(
-            st, zf, vs, rows, lane,
-            [&](int u, int k, uint32_t (&f)[4]) {
-              to_f16<FMT>(word(kx[u][k / 4], k % 4), f[0], f[2]);
-              to_f16<FMT>(word(kx[u][KJ + k / 4], k % 4), f[1], f[3]);
+        float zf[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) zf[nt][j] = zq[nt][j] * cur.ks;
+        tile_math<D, HM, true, true>(
+            st, zf, cur.vs, kPage, lane,
+            [&](int k, uint32_t (&f)[4]) {
+              to_f16<FMT>(word(kx[k / 4], k % 4), f[0], f[2]);
+              to_f16<FMT>(word(kx[KJ + k / 4], k % 4), f[1], f[3]);
             },
-            q_regs, v_load,
-            [&](int u, int k, uint32_t (&f)[4]) {
+            q_regs, next_k,
+            [&](int k, uint32_t (&f)[4]) {
               // the two tokens' bytes of column d, then of column d + 1
               const uint32_t sel = k % 2 ? 0x7362 : 0x5140;
               const int w = k / 2;
-              to_f16<FMT>(__byte_perm(word(vx[u][0], w), word(vx[u][1], w), sel), f[0], f[1]);
-              to_f16<FMT>(__byte_perm(word(vx[u][2], w), word(vx[u][3], w), sel), f[2], f[3]);
+              to_f16<FMT>(__byte_perm(word(vx[0], w), word(vx[1], w), sel), f[0], f[1]);
+              to_f16<FMT>(__byte_perm(word(vx[2], w), word(vx[3], w), sel), f[2], f[3]);
             });
       }
+    } else {
+      next_k();
     }
-    if (FMT != kBf16 && tail) {
+    if (FMT != kBf16 && cur.page == -2) {
       // the bf16 rows of the page that is not full, straight from memory, in
-      // the column orders of the 8-bit fragments; once for each listing
+      // the column orders of the 8-bit fragments
       const __nv_bfloat16* kt = a.k_tail + (size_t)bh * (kPage * D);
       const __nv_bfloat16* vt = a.v_tail + (size_t)bh * (kPage * D);
-      float zt[1][NT][2];
+      const int tail_rows = cur.rows;
+      float zt[NT][2];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) zt[0][nt][0] = zt[0][nt][1] = a.scale_log2;
-      const float one[1] = {1.f};
-      const int trows[1] = {tail_rows};
-      for (int u = 0; u < TP; ++u) {
-        if (meta[(i % S) * TP + u].page != -2) continue;
-        tile_math<D, HM, false, true, 1>(
-            st, zt, one, trows, lane,
-            [&](int, int k, uint32_t (&f)[4]) {
+      for (int nt = 0; nt < NT; ++nt) zt[nt][0] = zt[nt][1] = a.scale_log2;
+        tile_math<D, HM, false, true>(
+            st, zt, 1.f, tail_rows, lane,
+            [&](int k, uint32_t (&f)[4]) {
               const int d = (t + 4 * (k / 4)) * 16 + (k % 4) * 4;
               uint2 x = make_uint2(0, 0), y = make_uint2(0, 0);
               if (g < tail_rows) x = __ldg(reinterpret_cast<const uint2*>(kt + g * D + d));
@@ -714,7 +629,7 @@ __device__ __forceinline__ void attend_row(const PageAttnArgs& a, uint8_t* smem,
               b1 = x.y;
             },
             []() {},
-            [&](int, int k, uint32_t (&f)[4]) {
+            [&](int k, uint32_t (&f)[4]) {
               const int d = g * (D / 8) + 2 * k;
               uint32_t x[4];
 #pragma unroll
@@ -727,10 +642,10 @@ __device__ __forceinline__ void attend_row(const PageAttnArgs& a, uint8_t* smem,
               f[2] = __byte_perm(x[2], x[3], 0x5410);
               f[3] = __byte_perm(x[2], x[3], 0x7632);
             });
-      }
     }
+    if (nxt.page >= 0) load_v(nxt);
+    cur = nxt;
   }
-  cp_wait<0>();
 
   // Merge of the CTA's warps: O of each head, row of D floats padded by 8,
   // then (m, l) of each head.
@@ -740,7 +655,6 @@ __device__ __forceinline__ void attend_row(const PageAttnArgs& a, uint8_t* smem,
     for (int j = 0; j < 2; ++j)
 #pragma unroll
       for (int sh = 4; sh <= 16; sh <<= 1) st.l[nt][j] += __shfl_xor_sync(0xffffffffu, st.l[nt][j], sh);
-  __syncthreads();   // every warp is done with its ring
   constexpr int kLd = D + 8;
   float* so = reinterpret_cast<float*>(smem);
   float* sml = so + W * NT * 8 * kLd;
@@ -987,7 +901,7 @@ sfi_status run(const sfi_shape* shape, const sfi_paged_kv* kv, const sfi_quant_k
 // One wave of `per_sm` CTAs a multiprocessor, fewer where the tiles would not
 // give each kMinQuota.
 int page_attn_ctas(long long tiles, int per_sm) {
-  return (int)std::max(1LL, std::min((long long)num_sms() * per_sm, (tiles + kMinQuota - 1) / kMinQuota));
+  return (int)std::max(1LL, std::min((long long)num_sms() * per_sm * PA_WAVES, (tiles + kMinQuota - 1) / kMinQuota));
 }
 
 }  // namespace sfi
