@@ -367,7 +367,7 @@ sfi_status sfi_selftest_wait(const sfi_paged_kv* kv, int64_t limit_ns, sfi_strea
  * is latched as SFI_ERR_DEVICE_CHECK and its sequence treated as empty. */
 typedef enum { SFI_FMT_E4M3 = 0, SFI_FMT_INT8 = 1 } sfi_quant_format;
 
-/*  k_pool, v_pool    uint8 [num_pages, Hkv, 16, D]: codes, 16-byte aligned
+/*  k_pool, v_pool    uint8 [num_pages, Hkv, 16, D]: codes, 32-byte aligned
  *  k_scale, v_scale  fp32  [num_pages, Hkv]
  *  k_tail, v_tail    bf16  [B, Hkv, 16, D], 16-byte aligned: row r is token
  *                    16 * (len / 16) + r of the sequence while r < len % 16
@@ -481,7 +481,8 @@ sfi_status sfi_block_select(const sfi_shape* shape, const sfi_block_index* index
  * cache: the tokens below len of blocks sel[b, g, 0 .. K).  Entries outside
  * [0, ceil(len / 16)) are passed over; a block listed twice counts twice.  No
  * token left: out = 0, lse = -infinity.  The other arguments are those of
- * sfi_quant_attn.  sel_ld >= K >= 1. */
+ * sfi_quant_attn.  sel_ld >= K >= 1, K <= max_pages.  The bf16 pools must be
+ * 32-byte aligned here. */
 sfi_status sfi_block_attn(const sfi_shape* shape, const sfi_paged_kv* kv, int32_t L, const int32_t* lens,
                           const sfi_bf16* q, const int32_t* sel, int32_t sel_ld, int32_t K, float* out,
                           float* lse, void* ws, size_t ws_bytes, sfi_stream stream);

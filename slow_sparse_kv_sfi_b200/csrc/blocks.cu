@@ -14,24 +14,31 @@
 // its fragment straight from global memory: the order of d inside the dot
 // product is free as long as q uses the same one, so thread t of a quad takes
 // the 16-byte chunks t, t + 4, ... of its two rows.
+#include <cooperative_groups.h>
+
 #include "common.cuh"
 #include "internal.h"
 
 namespace sfi {
 namespace {
 
-constexpr int kScoreWarps = 8;
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+constexpr int kMaxRow = 16384;       // blocks a row's keys take in one CTA's shared memory (64 KB)
+constexpr int kMaxCluster = 8;
 
-struct BlockScoreArgs {
+struct SelectArgs {
   int B, Hq, Hkv, G, L, num_pages, max_pages, nb;
-  int n_sink, n_recent;
+  int n_sink, n_recent, K;
   const int32_t* lens;
   const __nv_bfloat16* q;
   const int8_t* bounds;
   const float* scale;
   const int32_t* pt;
-  float* scores;
+  float* scores;     // [B * Hkv][ld] (score kernel)
   int64_t ld;
+  int32_t* sel;      // [B * Hkv][sel_ld] (select kernel)
+  int64_t sel_ld;
   int* err;
 };
 
@@ -48,17 +55,20 @@ __device__ __forceinline__ float tame(float x) {
   return x != x ? 0.f : fminf(fmaxf(x, -big), big);
 }
 
+// The group's query codes, as the B operands of the products ([column tile]
+// [16-byte chunk of a thread][lane]), and every head's scale.
 template <int D, int NT>
-__global__ void __launch_bounds__(kScoreWarps * 32) block_score_kernel(const BlockScoreArgs a) {
-  grid_dep_enter();
-  constexpr int KC = 2 * D / 64;   // 16-byte chunks per thread and row
-  __shared__ __align__(16) int8_t qc[NT * 8][2 * D];
-  __shared__ float qe[NT * 8];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int bh = blockIdx.y, b = bh / a.Hkv, h = bh - b * a.Hkv;
+struct Query {
+  uint4 b[NT][2 * D / 64][32];
+  float e[NT * 8];
+};
 
-  // the group's query codes, split by sign
-  for (int n = warp; n < NT * 8; n += kScoreWarps) {
+// Whole CTA.  Chunk c of lane (g, t) holds bytes (t + 4 c) * 16 ... of head
+// nt * 8 + g's 2 D codes [max(q^, 0) | min(q^, 0)].
+template <int D, int NT>
+__device__ __forceinline__ void load_query(const SelectArgs& a, int b, int h, Query<D, NT>& s) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int n = warp; n < NT * 8; n += kWarps) {
     constexpr int E = D / 32;
     float x[E];
     float am = 0.f;
@@ -74,83 +84,375 @@ __global__ void __launch_bounds__(kScoreWarps * 32) block_score_kernel(const Blo
 #pragma unroll
     for (int e = 0; e < E; ++e) {
       const int c = __float2int_rn(x[e] * inv);
-      qc[n][lane * E + e] = (int8_t)max(c, 0);
-      qc[n][D + lane * E + e] = (int8_t)min(c, 0);
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int at = half * D + lane * E + e;           // byte of the head's row of codes
+        const int chunk = at / 16, t = chunk % 4, j = chunk / 4;
+        reinterpret_cast<int8_t*>(&s.b[n / 8][j][(n % 8) * 4 + t])[at % 16] = (int8_t)(half ? min(c, 0) : max(c, 0));
+      }
     }
-    if (lane == 0) qe[n] = __uint_as_float((uint32_t)(ex + 127) << 23);
+    if (lane == 0) s.e[n] = __uint_as_float((uint32_t)(ex + 127) << 23);
   }
   __syncthreads();
+}
 
-  const int len = seq_len(a.lens, a.L, b, a.err);
-  const int r0 = lane >> 2, t = lane & 3;
-  uint32_t qb[NT][KC][4];
+// What lane (g, t) of a warp needs to know of blocks tile * 16 + g and
+// tile * 16 + 8 + g: the page whose bounds give the score, or (page < 0) the
+// score itself: -infinity past the end and for a bad page table entry,
+// +infinity for the blocks that are always taken.
+struct Where {
+  int page[2];
+  float fixed[2];
+};
+__device__ __forceinline__ Where locate(const SelectArgs& a, int b, int len, int tile, int lane) {
+  Where w;
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int j = 0; j < KC; ++j)
-#pragma unroll
-      for (int w = 0; w < 4; ++w)
-        qb[nt][j][w] = *reinterpret_cast<const uint32_t*>(&qc[nt * 8 + r0][(t + 4 * j) * 16 + 4 * w]);
-
-  const int n_tiles = (a.nb + 15) / 16;
-  for (int tile = blockIdx.x * kScoreWarps + warp; tile < n_tiles; tile += gridDim.x * kScoreWarps) {
-    uint4 x[2][KC];
-    float sc[2];
-    float forced[2];   // the score where it does not come from the bounds, else NaN
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int j = tile * 16 + r0 + 8 * r;
-      sc[r] = 0.f;
-      forced[r] = __uint_as_float(0x7fc00000u);
-#pragma unroll
-      for (int c = 0; c < KC; ++c) x[r][c] = make_uint4(0, 0, 0, 0);
-      if (j * kPage >= len) {
-        forced[r] = -INFINITY;
-      } else if (j * kPage < a.n_sink || (j + 1) * kPage > len - a.n_recent) {
-        forced[r] = INFINITY;
-      } else {
-        const int page = __ldg(a.pt + (size_t)b * a.max_pages + j);
-        if ((unsigned)page >= (unsigned)a.num_pages) {
-          latch_error(a.err, SFI_ERR_DEVICE_CHECK, kSiteBlockPage);
-          forced[r] = -INFINITY;
-        } else {
-          const size_t ph = (size_t)page * a.Hkv + h;
-          const uint4* row = reinterpret_cast<const uint4*>(a.bounds + ph * 2 * D);
-#pragma unroll
-          for (int c = 0; c < KC; ++c) x[r][c] = __ldg(row + t + 4 * c);
-          sc[r] = __ldg(a.scale + ph);
-        }
-      }
+  for (int r = 0; r < 2; ++r) {
+    const int j = tile * 16 + (lane >> 2) + 8 * r;
+    w.page[r] = -1;
+    w.fixed[r] = -INFINITY;
+    if ((long)j * kPage >= len) continue;
+    if (j * kPage < a.n_sink || (j + 1) * kPage > len - a.n_recent) {
+      w.fixed[r] = INFINITY;
+      continue;
     }
-    float best[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      int d[4] = {0, 0, 0, 0};
-#pragma unroll
-      for (int c = 0; c < KC; ++c) {
-        const uint32_t a0[4] = {x[0][c].x, x[1][c].x, x[0][c].y, x[1][c].y};
-        const uint32_t a1[4] = {x[0][c].z, x[1][c].z, x[0][c].w, x[1][c].w};
-        mma_s8_16832(d, a0, qb[nt][c][0], qb[nt][c][1]);
-        mma_s8_16832(d, a1, qb[nt][c][2], qb[nt][c][3]);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int n = nt * 8 + 2 * t + (i & 1);
-        if (n < a.G) best[i >> 1] = fmaxf(best[i >> 1], (float)d[i] * qe[n]);
-      }
-    }
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      best[r] = fmaxf(best[r], __shfl_xor_sync(0xffffffffu, best[r], 1));
-      best[r] = fmaxf(best[r], __shfl_xor_sync(0xffffffffu, best[r], 2));
-      const int j = tile * 16 + r0 + 8 * r;
-      if (t == r && j < a.nb) {
-        const float big = __uint_as_float(0x7f7fffffu);
-        const float u = fminf(fmaxf(best[r] * sc[r], -big), big);
-        a.scores[(size_t)bh * a.ld + j] = forced[r] == forced[r] ? forced[r] : u;
-      }
+    w.page[r] = __ldg(a.pt + (size_t)b * a.max_pages + j);
+    if ((unsigned)w.page[r] >= (unsigned)a.num_pages) {
+      latch_error(a.err, SFI_ERR_DEVICE_CHECK, kSiteBlockPage);
+      w.page[r] = -1;
     }
   }
+  return w;
+}
+
+// Scores of a tile for KV head h, by one warp: lanes with t = 0 return block
+// tile * 16 + g, lanes with t = 1 block tile * 16 + 8 + g.
+template <int D, int NT>
+__device__ __forceinline__ float score_tile(const SelectArgs& a, int h, const Where& w, int lane,
+                                            const Query<D, NT>& s) {
+  constexpr int KC = 2 * D / 64;
+  const int t = lane & 3;
+  uint4 x[2][KC];
+  float sc[2];
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    sc[r] = 0.f;
+#pragma unroll
+    for (int c = 0; c < KC; ++c) x[r][c] = make_uint4(0, 0, 0, 0);
+    if (w.page[r] < 0) continue;
+    const size_t ph = (size_t)w.page[r] * a.Hkv + h;
+    const uint4* row = reinterpret_cast<const uint4*>(a.bounds + ph * 2 * D);
+#pragma unroll
+    for (int c = 0; c < KC; ++c) x[r][c] = __ldg(row + t + 4 * c);
+    sc[r] = __ldg(a.scale + ph);
+  }
+  float best[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    int d[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int c = 0; c < KC; ++c) {
+      const uint4 q = s.b[nt][c][lane];
+      const uint32_t a0[4] = {x[0][c].x, x[1][c].x, x[0][c].y, x[1][c].y};
+      const uint32_t a1[4] = {x[0][c].z, x[1][c].z, x[0][c].w, x[1][c].w};
+      mma_s8_16832(d, a0, q.x, q.y);
+      mma_s8_16832(d, a1, q.z, q.w);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int n = nt * 8 + 2 * t + (i & 1);
+      if (n < a.G) best[i >> 1] = fmaxf(best[i >> 1], (float)d[i] * s.e[n]);
+    }
+  }
+  const float big = __uint_as_float(0x7f7fffffu);
+  float u[2];
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    best[r] = fmaxf(best[r], __shfl_xor_sync(0xffffffffu, best[r], 1));
+    best[r] = fmaxf(best[r], __shfl_xor_sync(0xffffffffu, best[r], 2));
+    u[r] = w.page[r] >= 0 ? fminf(fmaxf(best[r] * sc[r], -big), big) : w.fixed[r];
+  }
+  return t == 0 ? u[0] : u[1];
+}
+
+// Scores alone, for rows that the select kernel does not hold.
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads, 2) block_score_kernel(const SelectArgs a) {
+  grid_dep_enter();
+  __shared__ Query<D, NT> s;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int bh = blockIdx.y, b = bh / a.Hkv, h = bh - b * a.Hkv;
+  load_query<D, NT>(a, b, h, s);
+  const int len = seq_len(a.lens, a.L, b, a.err);
+  const int n_tiles = (a.nb + 15) / 16;
+  Where w = locate(a, b, len, blockIdx.x * kWarps + warp, lane);
+  for (int tile = blockIdx.x * kWarps + warp; tile < n_tiles; tile += gridDim.x * kWarps) {
+    const Where next = locate(a, b, len, tile + gridDim.x * kWarps, lane);
+    const float u = score_tile<D, NT>(a, h, w, lane, s);
+    w = next;
+    const int j = tile * 16 + (lane >> 2) + 8 * (lane & 1);
+    if ((lane & 2) == 0 && j < a.nb) a.scores[(size_t)bh * a.ld + j] = u;
+  }
+}
+
+// A key back to its score (the inverse of float_key).
+__device__ __forceinline__ float key_score(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k);
+}
+
+constexpr uint32_t kForced = 0xffffffffu;   // key of a block that is always taken (float_key gives less)
+constexpr int kBins = 4 * kThreads;
+
+struct Search {
+  uint32_t cnt[2][kWarps][4];
+  int2 scan[kWarps];
+  int hist[kBins];
+  uint32_t cand[kThreads];
+  int bin, above, m;
+  uint32_t threshold;
+};
+
+// The K-th largest of keys[0, n), n > K, by the whole CTA, or any value that
+// splits off K keys.  A histogram over kBins equal steps of the score gives the
+// bin of the K-th largest; of its few keys each thread ranks one.  A bin that
+// holds more than kThreads keys (equal or very uneven scores) is left to a
+// bisection over the keys: three thresholds a round, counted by the whole CTA.
+__device__ __forceinline__ uint32_t kth_key(const uint32_t* keys, int n, int K, Search& s) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // forced blocks, smallest and largest other key
+  uint32_t mn = kForced, mx = 0u, forced = 0u;
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    const uint32_t k = keys[i];
+    forced += k == kForced;
+    mn = min(mn, k);
+    mx = max(mx, k == kForced ? 0u : k);
+  }
+  mn = __reduce_min_sync(0xffffffffu, mn);
+  mx = __reduce_max_sync(0xffffffffu, mx);
+  forced = __reduce_add_sync(0xffffffffu, forced);
+  if (lane == 0) *reinterpret_cast<uint4*>(s.cnt[0][warp]) = make_uint4(mn, mx, forced, 0u);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) s.hist[i * kThreads + threadIdx.x] = 0;
+  if (threadIdx.x == 0) s.m = 0;
+  __syncthreads();
+  uint32_t lo = kForced, hi = 0u;
+  forced = 0u;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    const uint4 v = *reinterpret_cast<const uint4*>(s.cnt[0][w]);
+    lo = min(lo, v.x);
+    hi = max(hi, v.y);
+    forced += v.z;
+  }
+  const int need = K - (int)forced;
+  if (need <= 0) return kForced - 1u;   // the forced ones are all
+  // monotone in the score; a range that overflows puts all into one bin, and
+  // -infinity (a bad page) goes to the lowest
+  const float s0 = fmaxf(key_score(lo), -3.402823466e38f);
+  const float step = __fdiv_rn((float)kBins, key_score(hi) - s0);
+  auto bin_of = [&](uint32_t k) { return max(0, min(kBins - 1, (int)((key_score(k) - s0) * step))); };
+  for (int i = threadIdx.x; i < n; i += kThreads)
+    if (keys[i] != kForced) atomicAdd(&s.hist[bin_of(keys[i])], 1);
+  __syncthreads();
+  // sums from the top: thread t owns bins kBins - 4 t - 1 down to kBins - 4 t - 4
+  int own[4], sum = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    own[i] = s.hist[kBins - 1 - 4 * (int)threadIdx.x - i];
+    sum += own[i];
+  }
+  int x = sum;
+#pragma unroll
+  for (int sh = 1; sh < 32; sh <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, sh);
+    if (lane >= sh) x += y;
+  }
+  if (lane == 31) s.scan[warp].x = x;
+  __syncthreads();
+  int above = x - sum;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) above += w < warp ? s.scan[w].x : 0;
+  if (above < need && above + sum >= need) {   // one thread
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (above < need && above + own[i] >= need) {
+        s.bin = kBins - 1 - 4 * (int)threadIdx.x - i;
+        s.above = above;
+      }
+      above += own[i];
+    }
+  }
+  __syncthreads();
+  const int bin = s.bin;
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    const uint32_t k = keys[i];
+    if (k != kForced && bin_of(k) == bin) {
+      const int at = atomicAdd(&s.m, 1);
+      if (at < kThreads) s.cand[at] = k;
+    }
+  }
+  __syncthreads();
+  const int m = s.m;
+  if (m <= kThreads) {
+    const int rank = need - s.above;   // the rank-th largest of the bin
+    if ((int)threadIdx.x < m) {
+      const uint32_t k = s.cand[threadIdx.x];
+      int gt = 0, ge = 0;
+      for (int i = 0; i < m; ++i) {
+        gt += s.cand[i] > k;
+        ge += s.cand[i] >= k;
+      }
+      if (gt < rank && ge >= rank) s.threshold = k;   // equal keys write the same
+    }
+    __syncthreads();
+    return s.threshold;
+  }
+  // bisection: at least K keys are >= lo, and at most the forced ones > hi
+  for (int round = 1; lo < hi; ++round) {
+    const uint32_t d = hi - lo;
+    // lo < m0 <= m1 <= m2 <= hi
+    const uint32_t m0 = lo + (d >> 2) + 1, m1 = max(m0, lo + (d >> 1) + 1), m2 = max(m1, lo + (d >> 1) + (d >> 2) + 1);
+    uint32_t c0 = 0, c1 = 0, c2 = 0;
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+      const uint32_t k = keys[i];
+      c0 += k >= m0;
+      c1 += k >= m1;
+      c2 += k >= m2;
+    }
+    c0 = __reduce_add_sync(0xffffffffu, c0);
+    c1 = __reduce_add_sync(0xffffffffu, c1);
+    c2 = __reduce_add_sync(0xffffffffu, c2);
+    if (lane == 0) *reinterpret_cast<uint4*>(s.cnt[round & 1][warp]) = make_uint4(c0, c1, c2, 0u);
+    __syncthreads();   // the readers of this buffer's last use are past the last round's barrier
+    c0 = c1 = c2 = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const uint4 v = *reinterpret_cast<const uint4*>(s.cnt[round & 1][w]);
+      c0 += v.x;
+      c1 += v.y;
+      c2 += v.z;
+    }
+    uint32_t c;
+    if (c2 >= (uint32_t)K) {
+      lo = m2;
+      c = c2;
+    } else if (c1 >= (uint32_t)K) {
+      lo = m1;
+      hi = m2 - 1;
+      c = c1;
+    } else if (c0 >= (uint32_t)K) {
+      lo = m0;
+      hi = m1 - 1;
+      c = c0;
+    } else {
+      hi = m0 - 1;
+      c = 0;
+    }
+    if (c == (uint32_t)K) break;   // lo splits off K keys
+  }
+  return lo;
+}
+
+// Scores and selection of one row by a cluster of CTAs: all of them score a
+// share of the row's blocks into the first one's shared memory, which then
+// finds the K-th largest key and writes the chosen blocks in order.
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads, 2) block_select_kernel(const SelectArgs a) {
+  grid_dep_wait();
+  namespace cg = cooperative_groups;
+  cg::cluster_group cl = cg::this_cluster();
+  extern __shared__ __align__(16) uint32_t keys[];   // of the cluster's first CTA
+  __shared__ union Shared {
+    Query<D, NT> query;
+    Search search;
+  } sh;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int cs = (int)cl.num_blocks(), rank = (int)cl.block_rank();
+  const int bh = blockIdx.x / cs, b = bh / a.Hkv, h = bh - b * a.Hkv;
+  int32_t* out = a.sel + (size_t)bh * a.sel_ld;
+  const int len = seq_len(a.lens, a.L, b, rank == 0 && threadIdx.x == 0 ? a.err : nullptr);
+  const int n = (len + kPage - 1) / kPage;
+  if (n <= a.K) {   // the same in every CTA of the cluster
+    if (rank == 0)
+      for (int i = threadIdx.x; i < a.K; i += kThreads) out[i] = i;
+    return;
+  }
+  Where w = locate(a, b, len, rank * kWarps + warp, lane);
+  load_query<D, NT>(a, b, h, sh.query);
+  uint32_t* first = cl.map_shared_rank(keys, 0);
+  cl.sync();   // the first CTA runs, so its shared memory may be written
+  for (int tile = rank * kWarps + warp; tile * 16 < n; tile += cs * kWarps) {
+    const Where next = locate(a, b, len, tile + cs * kWarps, lane);
+    const float u = score_tile<D, NT>(a, h, w, lane, sh.query);
+    w = next;
+    const int j = tile * 16 + (lane >> 2) + 8 * (lane & 1);
+    if ((lane & 2) == 0 && j < n) first[j] = u == INFINITY ? kForced : float_key(u);
+  }
+  cl.sync();
+  if (rank != 0) return;
+  const uint32_t lo = kth_key(keys, n, a.K, sh.search);
+  __syncthreads();   // its shared memory is used again
+  int2* scan = sh.search.scan;
+
+  // All keys above lo, and the first of those equal to it.  Warp w takes the w-th run of positions,
+  // 32 at a time, so the chosen ones come out in order.
+  const int run = (n + 32 * kWarps - 1) / (32 * kWarps) * 32;
+  const int i0 = min(n, warp * run), i1 = min(n, i0 + run);
+  int above = 0, equal = 0;
+  for (int i = i0 + lane; i - lane < i1; i += 32) {
+    const uint32_t k = i < i1 ? keys[i] : 0u;
+    above += __popc(__ballot_sync(0xffffffffu, i < i1 && k > lo));
+    equal += __popc(__ballot_sync(0xffffffffu, i < i1 && k == lo));
+  }
+  if (lane == 0) scan[warp] = make_int2(above, equal);
+  __syncthreads();
+  int total = 0;
+  above = equal = 0;   // of the positions before this warp's run
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    const int2 v = scan[w];
+    total += v.x;
+    above += w < warp ? v.x : 0;
+    equal += w < warp ? v.y : 0;
+  }
+  const int take = a.K - total;   // how many of the equal ones
+  for (int i = i0 + lane; i - lane < i1; i += 32) {
+    const uint32_t k = i < i1 ? keys[i] : 0u;
+    const uint32_t below = (1u << lane) - 1u;
+    const uint32_t ma = __ballot_sync(0xffffffffu, i < i1 && k > lo);
+    const uint32_t me = __ballot_sync(0xffffffffu, i < i1 && k == lo);
+    const int eq = equal + __popc(me & below);
+    const bool chosen = (ma >> lane & 1u) || ((me >> lane & 1u) && eq < take);
+    if (chosen) out[above + __popc(ma & below) + min(eq, take)] = i;
+    above += __popc(ma);
+    equal += __popc(me);
+  }
+}
+
+template <int D, int NT>
+cudaError_t launch_select(const SelectArgs& a, int BH, int cs, cudaStream_t st) {
+  const size_t smem = (size_t)((a.nb + 3) / 4 * 4) * sizeof(uint32_t);
+  auto k = block_select_kernel<D, NT>;
+  static DeviceOnce once;
+  if (!once.done()) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxRow * (int)sizeof(uint32_t));
+    if (!once.mark(e)) return e;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(BH * cs);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cs;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, k, a);
 }
 
 #define SFI_TRY(x)               \
@@ -205,7 +507,7 @@ sfi_status sfi_block_select(const sfi_shape* shape, const sfi_block_index* index
   const BlockWs w = block_ws(*shape);
   if (!ws || !aligned16(ws) || ws_bytes < w.total) return SFI_ERR_WORKSPACE;
   const int BH = shape->B * shape->Hkv;
-  BlockScoreArgs a{};
+  SelectArgs a{};
   a.B = shape->B;
   a.Hq = shape->Hq;
   a.Hkv = shape->Hkv;
@@ -216,6 +518,7 @@ sfi_status sfi_block_select(const sfi_shape* shape, const sfi_block_index* index
   a.nb = nb;
   a.n_sink = n_sink;
   a.n_recent = n_recent;
+  a.K = K;
   a.lens = lens;
   a.q = reinterpret_cast<const __nv_bfloat16*>(q);
   a.bounds = index->bounds;
@@ -223,22 +526,33 @@ sfi_status sfi_block_select(const sfi_shape* shape, const sfi_block_index* index
   a.pt = index->page_table;
   a.scores = reinterpret_cast<float*>(static_cast<char*>(ws) + w.score_off);
   a.ld = (nb + 3) / 4 * 4;
+  a.sel = sel;
+  a.sel_ld = sel_ld;
   a.err = index->err;
   cudaStream_t st = (cudaStream_t)stream;
-  // one tile of 16 pages per warp until the grid fills the GPU about twice
-  // (256-thread CTAs, several per SM); longer rows loop
-  const int tiles = (nb + 15) / 16;
-  int gx = (tiles + kScoreWarps - 1) / kScoreWarps;
-  const int cap = (num_sms() * 8 + BH - 1) / BH;
-  if (gx > cap) gx = cap;
-  const dim3 grid(gx, BH);
   const bool wide = a.G > 8;
-  auto k = shape->D == 128 ? (wide ? block_score_kernel<128, 2> : block_score_kernel<128, 1>)
-                           : (wide ? block_score_kernel<64, 2> : block_score_kernel<64, 1>);
-  if (launch_k(k, grid, dim3(kScoreWarps * 32), 0, st, a) != cudaSuccess) {
+  cudaError_t e;
+  if (nb <= kMaxRow) {
+    // one launch: a cluster per row, as many CTAs as keep the GPU at two each
+    // multiprocessor and leave every warp a tile
+    int cs = 1;
+    while (cs < kMaxCluster && 2L * cs * BH <= 2L * num_sms() && cs * kWarps * 16 < nb) cs *= 2;
+    e = shape->D == 128 ? (wide ? launch_select<128, 2>(a, BH, cs, st) : launch_select<128, 1>(a, BH, cs, st))
+                        : (wide ? launch_select<64, 2>(a, BH, cs, st) : launch_select<64, 1>(a, BH, cs, st));
+  } else {
+    const int tiles = (nb + 15) / 16;
+    int gx = (tiles + kWarps - 1) / kWarps;
+    const int cap = (num_sms() * 4 + BH - 1) / BH;
+    if (gx > cap) gx = cap;
+    auto k = shape->D == 128 ? (wide ? block_score_kernel<128, 2> : block_score_kernel<128, 1>)
+                             : (wide ? block_score_kernel<64, 2> : block_score_kernel<64, 1>);
+    e = launch_k(k, dim3(gx, BH), dim3(kThreads), 0, st, a);
+  }
+  if (e != cudaSuccess) {
     cudaGetLastError();
     return SFI_ERR_CUDA;
   }
+  if (nb <= kMaxRow) return SFI_OK;
   return run_topk(BH, nb, a.scores, a.ld, K, 0, sel, sel_ld, nullptr, 0, st);
 }
 

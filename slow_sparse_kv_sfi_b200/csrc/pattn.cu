@@ -100,11 +100,21 @@ struct Cfg {
   static constexpr int kEl = FMT == kBf16 ? 2 : 1;
   static constexpr int kRow = D * kEl;                  // bytes of a row
   static constexpr int KJ = kRow / 64;                  // 16-byte pieces of a K row per thread
+  static constexpr int KL = kRow >= 128 ? 32 : 16;      // bytes of a load of them
   static constexpr int kVB = kRow / 8;                  // bytes of a V row per thread: 8, 16 or 32
   static constexpr int VC = kVB >= 16 ? kVB / 16 : 1;   // pieces of them
-  static constexpr int VP = kVB >= 16 ? 16 : 8;         // bytes of a piece
   static constexpr int kTile = 16 * kRow;               // bytes of a tile of K, and of V
+  // First of the four columns that thread t of a quad contributes to step k of
+  // S^T, and of the two that thread g contributes to m tile k of O^T.
+  static __device__ __forceinline__ int k_col(int t, int k) {
+    return kEl == 2 ? (k / 4) * 64 + t * 16 + (k % 4) * 4 : KJ == 2 ? t * 32 + k * 4 : t * 16 + k * 4;
+  }
+  static __device__ __forceinline__ int v_col(int g, int k) { return g * (D / 8) + 2 * k; }
   static constexpr int W = NT == 2 ? PA_W2 : FMT == kBf16 ? PA_WB : PA_W;   // warps
+  // Tiles fetched into L2 ahead of their loads: one for 8-bit pages (a warp's
+  // registers hold one 4 KB tile in flight, less than the latency asks for);
+  // none for bf16 pages, whose tile is twice as large.
+  static constexpr int kAhead = FMT == kBf16 ? 0 : 1;
   static constexpr int kCtas = NT == 2 ? 2 : PA_CT;                   // per SM
   static constexpr int kSmem = W * NT * 8 * (D + 8) * 4 + W * NT * 8 * 2 * 4;   // merge of the warps
 };
@@ -195,6 +205,11 @@ __device__ __forceinline__ uint4 ld16(const uint8_t* p) {
                : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
                : "l"(p));
   return r;
+}
+__device__ __forceinline__ void ld32(const uint8_t* p, uint4& x, uint4& y) {
+  asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w), "=r"(y.x), "=r"(y.y), "=r"(y.z), "=r"(y.w)
+               : "l"(p));
 }
 __device__ __forceinline__ uint4 ld8(const uint8_t* p) {
   uint4 r = make_uint4(0, 0, 0, 0);
@@ -412,7 +427,7 @@ template <int D, int FMT, int HM, bool LIST>
 __device__ __forceinline__ void attend_row(const PageAttnArgs& a, uint8_t* smem, int b, int h, int len, int T, int t0,
                                            int t1) {
   using C = Cfg<D, FMT, HM>;
-  constexpr int NT = C::NT, W = C::W, KJ = C::KJ, VC = C::VC, VP = C::VP;
+  constexpr int NT = C::NT, W = C::W, KJ = C::KJ, VC = C::VC;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const int bh = b * a.Hkv + h;
@@ -426,40 +441,17 @@ __device__ __forceinline__ void attend_row(const PageAttnArgs& a, uint8_t* smem,
   float zq[NT][2];
   auto q_at = [&](int nt, int k) {   // four columns of the head of column nt * 8 + g
     const int n = HM == kHalf ? g & 3 : nt * 8 + g;
-    const int d = FMT == kBf16 ? (t + 4 * (k / 2)) * 8 + (k % 2) * 4 : (t + 4 * (k / 4)) * 16 + (k % 4) * 4;
     if (n >= a.G) return make_uint2(0, 0);
-    return __ldg(reinterpret_cast<const uint2*>(a.q + ((size_t)b * a.Hq + h * a.G + n) * D + d));
+    return __ldg(reinterpret_cast<const uint2*>(a.q + ((size_t)b * a.Hq + h * a.G + n) * D + C::k_col(t, k)));
   };
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    uint32_t am = 0;
+  for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int k = 0; k < D / 16; ++k) {
       const uint2 x = q_at(nt, k);
       qb[nt][k][0] = x.x;
       qb[nt][k][1] = x.y;
-      am = __vmaxu2(am, __vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu));
     }
-    zq[nt][0] = zq[nt][1] = a.scale_log2;
-    if constexpr (FMT != kBf16) {
-      am = max(am & 0xffffu, am >> 16);
-      am = max(am, __shfl_xor_sync(0xffffffffu, am, 1));
-      am = max(am, __shfl_xor_sync(0xffffffffu, am, 2));
-      // biased exponent of the head's largest value; up = 2^(14 - exponent)
-      const int e = (int)(am >> 7);
-      const int up = e == 0xff || am == 0 ? 127 : min(127 + 14 - (e - 127), 253);
-      const float f = __uint_as_float((uint32_t)up << 23), inv = __uint_as_float((uint32_t)(254 - up) << 23);
-#pragma unroll
-      for (int k = 0; k < D / 16; ++k)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float2 x = unpack_bf16x2(qb[nt][k][i]);
-          qb[nt][k][i] = pack_f16x2(x.x * f, x.y * f);
-        }
-#pragma unroll
-      for (int j = 0; j < 2; ++j) zq[nt][j] *= __shfl_sync(0xffffffffu, inv, (2 * t + j) * 4);
-    }
-  }
 
   // Tiles of this warp: t0 + warp + W * i, i < n.  Lane l looks up tile i0 + l of
   // a batch of 32: block, page and scales.
@@ -490,10 +482,24 @@ __device__ __forceinline__ void attend_row(const PageAttnArgs& a, uint8_t* smem,
     }
   };
 
+  // The warp brings a tile into L2 kAhead tiles before it loads it.
+  auto fetch = [&](int j) {
+    const int page = __shfl_sync(0xffffffffu, mine.page, j);
+    if (page < 0) return;
+    const size_t off = ((size_t)page * a.Hkv + h) * C::kTile;
+#pragma unroll
+    for (int o = (lane & 15) * 128; o < C::kTile; o += 2048)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"((lane < 16 ? a.k : a.v) + off + o));
+  };
   auto tile_at = [&](int i) {
     Tile x{-1, 0, 0.f, 0.f};
     if (i >= n) return x;
-    if ((i & 31) == 0) look_up(i);
+    if ((i & 31) == 0) {
+      look_up(i);
+      for (int j = 1; j <= C::kAhead; ++j) fetch(j);
+    } else if (C::kAhead > 0 && (i & 31) + C::kAhead < 32) {
+      fetch((i & 31) + C::kAhead);
+    }
     x.page = __shfl_sync(0xffffffffu, mine.page, i & 31);
     x.rows = __shfl_sync(0xffffffffu, mine.rows, i & 31);
     if (FMT != kBf16) {
@@ -503,26 +509,39 @@ __device__ __forceinline__ void attend_row(const PageAttnArgs& a, uint8_t* smem,
     return x;
   };
   uint4 kx[2 * KJ], vx[4 * VC];
-  const uint8_t* k0 = a.k + (size_t)h * C::kTile + g * C::kRow + t * 16;
-  const uint8_t* v0 = a.v + (size_t)h * C::kTile + 2 * t * C::kRow + g * VP;
+  const uint8_t* k0 = a.k + (size_t)h * C::kTile + g * C::kRow + t * C::KL;
+  const uint8_t* v0 = a.v + (size_t)h * C::kTile + 2 * t * C::kRow + g * C::kVB;
   auto load_k = [&](const Tile& x) {
     const uint8_t* p = k0 + (size_t)x.page * a.Hkv * C::kTile;
 #pragma unroll
-    for (int r = 0; r < 2; ++r)
+    for (int r = 0; r < 2; ++r) {
+      const uint8_t* at = p + r * 8 * C::kRow;
+      if (FMT == kBf16 && g + 8 * r >= x.rows) {
 #pragma unroll
-      for (int j = 0; j < KJ; ++j)
-        kx[r * KJ + j] = FMT != kBf16 || g + 8 * r < x.rows ? ld16(p + r * 8 * C::kRow + j * 64) : make_uint4(0, 0, 0, 0);
+        for (int j = 0; j < KJ; ++j) kx[r * KJ + j] = make_uint4(0, 0, 0, 0);
+      } else if constexpr (C::KL == 32) {
+#pragma unroll
+        for (int j = 0; j < KJ; j += 2) ld32(at + j * 64, kx[r * KJ + j], kx[r * KJ + j + 1]);
+      } else {
+        kx[r] = ld16(at);
+      }
+    }
   };
   auto load_v = [&](const Tile& x) {
     const uint8_t* p = v0 + (size_t)x.page * a.Hkv * C::kTile;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int tok = (i & 1) + 8 * (i >> 1);
+      const uint8_t* at = p + tok * C::kRow;
+      if (FMT == kBf16 && 2 * t + tok >= x.rows) {
 #pragma unroll
-      for (int c = 0; c < VC; ++c) {
-        const uint8_t* at = p + tok * C::kRow + c * 128;
-        if constexpr (VP == 8) vx[i] = ld8(at);
-        else vx[i * VC + c] = FMT != kBf16 || 2 * t + tok < x.rows ? ld16(at) : make_uint4(0, 0, 0, 0);
+        for (int c = 0; c < VC; ++c) vx[i * VC + c] = make_uint4(0, 0, 0, 0);
+      } else if constexpr (C::kVB == 32) {
+        ld32(at, vx[2 * i], vx[2 * i + 1]);
+      } else if constexpr (C::kVB == 16) {
+        vx[i] = ld16(at);
+      } else {
+        vx[i] = ld8(at);
       }
     }
   };
@@ -552,6 +571,34 @@ __device__ __forceinline__ void attend_row(const PageAttnArgs& a, uint8_t* smem,
     load_k(cur);
     load_v(cur);
   }
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    uint32_t am = 0;
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k) {
+      am = __vmaxu2(am, __vmaxu2(qb[nt][k][0] & 0x7fff7fffu, qb[nt][k][1] & 0x7fff7fffu));
+    }
+    zq[nt][0] = zq[nt][1] = a.scale_log2;
+    if constexpr (FMT != kBf16) {
+      am = max(am & 0xffffu, am >> 16);
+      am = max(am, __shfl_xor_sync(0xffffffffu, am, 1));
+      am = max(am, __shfl_xor_sync(0xffffffffu, am, 2));
+      // biased exponent of the head's largest value; up = 2^(14 - exponent)
+      const int e = (int)(am >> 7);
+      const int up = e == 0xff || am == 0 ? 127 : min(127 + 14 - (e - 127), 253);
+      const float f = __uint_as_float((uint32_t)up << 23), inv = __uint_as_float((uint32_t)(254 - up) << 23);
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float2 x = unpack_bf16x2(qb[nt][k][i]);
+          qb[nt][k][i] = pack_f16x2(x.x * f, x.y * f);
+        }
+#pragma unroll
+      for (int j = 0; j < 2; ++j) zq[nt][j] *= __shfl_sync(0xffffffffu, inv, (2 * t + j) * 4);
+    }
+  }
+
   for (int i = 0; i < n; ++i) {
     const Tile nxt = tile_at(i + 1);
     auto next_k = [&]() {
@@ -614,7 +661,7 @@ __device__ __forceinline__ void attend_row(const PageAttnArgs& a, uint8_t* smem,
         tile_math<D, HM, false, true>(
             st, zt, 1.f, tail_rows, lane,
             [&](int k, uint32_t (&f)[4]) {
-              const int d = (t + 4 * (k / 4)) * 16 + (k % 4) * 4;
+              const int d = C::k_col(t, k);
               uint2 x = make_uint2(0, 0), y = make_uint2(0, 0);
               if (g < tail_rows) x = __ldg(reinterpret_cast<const uint2*>(kt + g * D + d));
               if (g + 8 < tail_rows) y = __ldg(reinterpret_cast<const uint2*>(kt + (g + 8) * D + d));
@@ -630,7 +677,7 @@ __device__ __forceinline__ void attend_row(const PageAttnArgs& a, uint8_t* smem,
             },
             []() {},
             [&](int k, uint32_t (&f)[4]) {
-              const int d = g * (D / 8) + 2 * k;
+              const int d = C::v_col(g, k);
               uint32_t x[4];
 #pragma unroll
               for (int r = 0; r < 4; ++r) {
@@ -662,9 +709,7 @@ __device__ __forceinline__ void attend_row(const PageAttnArgs& a, uint8_t* smem,
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int k = 0; k < D / 16; ++k) {
-      int d;
-      if (FMT == kBf16) d = (k / 4) * 64 + g * 8 + (k % 4) * 2;
-      else d = g * (D / 8) + 2 * k;
+      const int d = C::v_col(g, k);
 #pragma unroll
       for (int j = 0; j < 2; ++j)
         *reinterpret_cast<float2*>(so + (size_t)(warp * NT * 8 + nt * 8 + 2 * t + j) * kLd + d) =
@@ -712,31 +757,33 @@ __global__ void __launch_bounds__(Cfg<D, FMT, HM>::W * 32, Cfg<D, FMT, HM>::kCta
   grid_dep_wait();
   grid_dep_launch();
 
-  // this CTA's run [pos, end) and the row it begins in
-  long long total, unused, pos, end, first;
-  int b;
-  count_tiles<LIST>(a, 0, lane, warp == 0 ? a.err : nullptr, total, unused);
-  pos = quota(total, a.ctas);
-  end = min(total, pos * (blockIdx.x + 1));
-  pos *= blockIdx.x;
-  if (pos >= end) return;
-  find_sequence<LIST>(a, pos, lane, b, first);
-
-  for (; pos < end; ++b) {   // sequences
+  // this CTA's run: `left` tiles from tile t0 of row (b, h) on
+  int b, h, t0, left;
+  {
+    long long total, unused, first;
+    count_tiles<LIST>(a, 0, lane, warp == 0 ? a.err : nullptr, total, unused);
+    const long long q = quota(total, a.ctas), pos = q * blockIdx.x;
+    if (pos >= total) return;
+    left = (int)min(q, total - pos);
+    find_sequence<LIST>(a, pos, lane, b, first);
+    const int T = row_tiles<LIST>(a, b, nullptr);
+    h = (int)((pos - first) / T);
+    t0 = (int)(pos - first - (long long)h * T);
+  }
+  for (; left > 0; ++b, h = 0) {   // sequences
     const int len = seq_len(a.lens, a.L, b, nullptr);
-    const int blocks = (len + kPage - 1) / kPage;
-    const int T = LIST ? a.K : blocks;
+    const int T = LIST ? a.K : (len + kPage - 1) / kPage;
     if (T == 0) continue;
-    for (int h = (int)((pos - first) / T); h < a.Hkv && pos < end; ++h) {   // rows
-      const int t0 = (int)(pos - first - (long long)h * T);
-      const int t1 = (int)min((long long)T, t0 + (end - pos));
+    for (; h < a.Hkv && left > 0; ++h) {   // rows
+      const int t1 = min(T, t0 + left);
       attend_row<D, FMT, HM, LIST>(a, smem, b, h, len, T, t0, t1);
-      pos += t1 - t0;
+      left -= t1 - t0;
+      t0 = 0;
       __syncthreads();   // the row's shared memory is free
     }
-    first += (long long)T * a.Hkv;
   }
 }
+
 // Merge of the pieces of a row for one query head: the CTAs whose runs the row
 // spans, D threads a piece, kGroups pieces at once.  Rows that one CTA finished
 // are passed over; rows without tiles get their empty result here.
@@ -819,6 +866,7 @@ sfi_status launch(PageAttnArgs& a, cudaStream_t st) {
   const int T = LIST ? a.K : (a.L + kPage - 1) / kPage;
   const long long total = (long long)a.B * a.Hkv * T;
   a.ctas = page_attn_ctas(total, C::kCtas);
+  if (quota(total, a.ctas) > 0x7fffffffLL) return SFI_ERR_SHAPE;
   const sfi_status r = cuda_status(launch_k(k, dim3(a.ctas), dim3(C::W * 32), C::kSmem, st, a));
   // no row is cut when every run is a whole number of rows of one length
   const bool cut = (!LIST && a.lens) || quota(total, a.ctas) % T != 0;
@@ -846,6 +894,10 @@ sfi_status run(const sfi_shape* shape, const sfi_paged_kv* kv, const sfi_quant_k
   SFI_TRY(q8 ? check_quant(q8) : check_kv(kv));
   SFI_TRY(check_L(shape, L));
   if (!q || !aligned16(q) || !out) return SFI_ERR_INVALID_ARG;
+  // the kernel loads the pools 32 bytes at a time
+  const uintptr_t pools = q8 ? reinterpret_cast<uintptr_t>(q8->k_pool) | reinterpret_cast<uintptr_t>(q8->v_pool)
+                             : reinterpret_cast<uintptr_t>(kv->k_pool) | reinterpret_cast<uintptr_t>(kv->v_pool);
+  if (pools & 31u) return SFI_ERR_INVALID_ARG;
   if (list) {
     if (!sel) return SFI_ERR_INVALID_ARG;
     if (K < 1 || sel_ld < K) return SFI_ERR_SHAPE;

@@ -388,8 +388,9 @@ sfi_status launched(cudaError_t e) {
 sfi_status check_quant(const sfi_quant_kv* q) {
   if (!q || !q->k_pool || !q->v_pool || !q->k_scale || !q->v_scale || !q->k_tail || !q->v_tail || !q->page_table)
     return SFI_ERR_INVALID_ARG;
-  if (!aligned16(q->k_pool) || !aligned16(q->v_pool) || !aligned16(q->k_tail) || !aligned16(q->v_tail))
+  if (((reinterpret_cast<uintptr_t>(q->k_pool) | reinterpret_cast<uintptr_t>(q->v_pool)) & 31u) != 0)
     return SFI_ERR_INVALID_ARG;
+  if (!aligned16(q->k_tail) || !aligned16(q->v_tail)) return SFI_ERR_INVALID_ARG;
   if (q->format != SFI_FMT_E4M3 && q->format != SFI_FMT_INT8) return SFI_ERR_UNSUPPORTED;
   return SFI_OK;
 }

@@ -189,15 +189,29 @@ def make_packed(k, v, pos, headmask, n_rows) -> Packed:
 
 def _arg(t, name, dtypes, shape=None):
     """Checks a tensor argument of the 8-bit and block calls and returns its address."""
+    if (t.dtype in dtypes and (shape is None or t.shape == shape) and t.is_contiguous()
+            and t.is_cuda and t.get_device() == torch.cuda.current_device()):
+        return t.data_ptr()
     if t.dtype not in dtypes:
         raise ValueError(f"{name}: dtype {t.dtype}, expected {' or '.join(str(d) for d in dtypes)}")
-    if shape is not None and tuple(t.shape) != shape:
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous")
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name}: must be on the current CUDA device, is on {t.device}")
-    return C.c_void_p(t.data_ptr())
+    raise ValueError(f"{name}: must be on the current CUDA device, is on {t.device}")
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _on(stream):
+    """The stream handle of a call: the given stream or the current one, read
+    without building a Stream object where torch allows it (3 us of a call)."""
+    if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
+        stream = torch.cuda.current_stream()
+    return stream.cuda_stream
 
 
 _BF16, _F32, _I32 = (torch.bfloat16,), (torch.float32,), (torch.int32,)
@@ -395,7 +409,7 @@ def sfi_selftest_wait(kv, limit_ns: int, stream=None):
 def sfi_quant_store(shape, kv, qkv, pos_lo, L, lens=None, index=None, stream=None):
     _dims(shape, qkv, index)
     _check(lib().sfi_quant_store(C.byref(shape), C.byref(kv), C.byref(qkv), _ref(index), pos_lo, L,
-                                 _lens(shape, lens), _stream(stream)), "sfi_quant_store")
+                                 _lens(shape, lens), _on(stream)), "sfi_quant_store")
 
 
 def sfi_quant_append(shape, qkv, L, k_new, v_new, lens=None, index=None, stream=None):
@@ -403,20 +417,20 @@ def sfi_quant_append(shape, qkv, L, k_new, v_new, lens=None, index=None, stream=
     tok = (shape.B, shape.Hkv, shape.D)
     _check(lib().sfi_quant_append(C.byref(shape), C.byref(qkv), _ref(index), L, _lens(shape, lens),
                                   _arg(k_new, "k_new", _BF16, tok), _arg(v_new, "v_new", _BF16, tok),
-                                  _stream(stream)), "sfi_quant_append")
+                                  _on(stream)), "sfi_quant_append")
 
 
 def sfi_quant_load(shape, qkv, kv, pos_lo, L, lens=None, stream=None):
     _dims(shape, qkv)
     _check(lib().sfi_quant_load(C.byref(shape), C.byref(qkv), C.byref(kv), pos_lo, L, _lens(shape, lens),
-                                _stream(stream)), "sfi_quant_load")
+                                _on(stream)), "sfi_quant_load")
 
 
 def sfi_quant_attn(shape, qkv, L, q, out, ws, lens=None, lse=None, stream=None):
     _dims(shape, qkv)
     q, out, lse = _attn_args(shape, q, out, lse)
     _check(lib().sfi_quant_attn(C.byref(shape), C.byref(qkv), L, _lens(shape, lens), q, out, lse, *_ws(ws),
-                                _stream(stream)), "sfi_quant_attn")
+                                _on(stream)), "sfi_quant_attn")
 
 
 def sfi_quant_poll_error(qkv) -> int:
@@ -428,7 +442,7 @@ def sfi_quant_poll_error(qkv) -> int:
 def sfi_block_build(shape, kv, index, pos_lo, L, lens=None, stream=None):
     _dims(shape, index)
     _check(lib().sfi_block_build(C.byref(shape), C.byref(kv), C.byref(index), pos_lo, L, _lens(shape, lens),
-                                 _stream(stream)), "sfi_block_build")
+                                 _on(stream)), "sfi_block_build")
 
 
 def sfi_block_workspace_size(shape: Shape) -> int:
@@ -442,14 +456,14 @@ def sfi_block_select(shape, index, L, q, n_sink, n_recent, K, sel, ws, lens=None
     _dims(shape, index)
     q = _arg(q, "q", _BF16, (shape.B, shape.Hq, shape.D))
     _check(lib().sfi_block_select(C.byref(shape), C.byref(index), L, _lens(shape, lens), q, n_sink, n_recent, K,
-                                  _sel(shape, sel), sel.shape[-1], *_ws(ws), _stream(stream)), "sfi_block_select")
+                                  _sel(shape, sel), sel.shape[-1], *_ws(ws), _on(stream)), "sfi_block_select")
 
 
 def sfi_block_attn(shape, kv, L, q, sel, K, out, ws, lens=None, lse=None, stream=None):
     """Attention over blocks sel[:, :, :K] of the bf16 cache."""
     q, out, lse = _attn_args(shape, q, out, lse)
     _check(lib().sfi_block_attn(C.byref(shape), C.byref(kv), L, _lens(shape, lens), q, _sel(shape, sel),
-                                sel.shape[-1], K, out, lse, *_ws(ws), _stream(stream)), "sfi_block_attn")
+                                sel.shape[-1], K, out, lse, *_ws(ws), _on(stream)), "sfi_block_attn")
 
 
 def sfi_quant_block_attn(shape, qkv, L, q, sel, K, out, ws, lens=None, lse=None, stream=None):
@@ -457,7 +471,7 @@ def sfi_quant_block_attn(shape, qkv, L, q, sel, K, out, ws, lens=None, lse=None,
     _dims(shape, qkv)
     q, out, lse = _attn_args(shape, q, out, lse)
     _check(lib().sfi_quant_block_attn(C.byref(shape), C.byref(qkv), L, _lens(shape, lens), q, _sel(shape, sel),
-                                      sel.shape[-1], K, out, lse, *_ws(ws), _stream(stream)), "sfi_quant_block_attn")
+                                      sel.shape[-1], K, out, lse, *_ws(ws), _on(stream)), "sfi_quant_block_attn")
 
 
 class Context:

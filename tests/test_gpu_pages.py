@@ -624,3 +624,41 @@ def test_restored_pages_feed_the_packed_path():
     assert c.error() == 0
     kc, vc = k2.cpu(), v2.cpu()
     check_all(c, lambda b, h, n: c.rows(kc, b, h, n), lambda b, h, n: c.rows(vc, b, h, n))
+
+
+@pytest.mark.parametrize("what", ["equal", "two values", "one far outlier", "zeros", "bad page"])
+@pytest.mark.parametrize("nb,K", [(700, 300), (5000, 700), (5000, 4999), (16384, 40)])
+def test_select_uneven_scores(what, nb, K):
+    """Score distributions that crowd one bin of the selection's histogram: all equal (ties to the
+    lower block), two values, an outlier far above the rest, zeros; and a page that cannot be read."""
+    D, n = 64, nb * PAGE
+    g = torch.Generator().manual_seed(3)
+    bounds = torch.zeros(nb, 1, 2, D, dtype=torch.int8)
+    scale = torch.ones(nb, 1)
+    q = torch.zeros(1, 1, D)
+    q[..., 0] = 127.0
+    if what == "equal":
+        bounds[:, :, 0, 0] = 5
+    elif what == "two values":
+        bounds[:, :, 0, 0] = torch.randint(0, 2, (nb, 1), generator=g).to(torch.int8) * 9
+    elif what == "one far outlier":
+        bounds[:, :, 0, 0] = torch.randint(-127, 128, (nb, 1), generator=g).to(torch.int8)
+        scale[nb // 2] = 2.0 ** 100
+    elif what == "bad page":
+        bounds[:, :, 0, 0] = torch.randint(-127, 128, (nb, 1), generator=g).to(torch.int8)
+    bounds[:, :, 1] = bounds[:, :, 0]
+    pt = torch.arange(nb, dtype=torch.int32).view(1, nb)
+    u = P.block_scores(q[0].double().numpy(), bounds[:, 0].numpy().astype(np.int64), scale[:, 0].double().numpy())
+    if what == "bad page":
+        pt[0, nb // 3] = -5
+        u[nb // 3] = -np.inf
+    shape = S.make_shape(1, 1, 1, D, nb, nb)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    d = [t.to(DEV).contiguous() for t in (bounds, scale, pt)]
+    ix = S.make_block_index(*d, err=err)
+    sel = torch.empty(1, 1, K, dtype=torch.int32, device=DEV)
+    ws = torch.empty(S.sfi_block_workspace_size(shape), dtype=torch.uint8, device=DEV)
+    S.sfi_block_select(shape, ix, n, q.to(torch.bfloat16).to(DEV), 4, 20, K, sel, ws)
+    torch.cuda.synchronize()
+    assert int(err.item()) == (5 | (14 << 8) if what == "bad page" else 0)
+    assert np.array_equal(sel[0, 0].cpu().numpy(), P.select(u, n, 4, 20, K))

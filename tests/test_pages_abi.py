@@ -19,7 +19,7 @@ def S():
 
 
 def _quant(S, **kw):
-    f = dict(k_pool=16, v_pool=16, k_scale=16, v_scale=16, k_tail=16, v_tail=16, page_table=16, err=None, format=0)
+    f = dict(k_pool=32, v_pool=32, k_scale=16, v_scale=16, k_tail=16, v_tail=16, page_table=16, err=None, format=0)
     f.update(kw)
     return S.QuantKV(**f)
 
@@ -45,7 +45,7 @@ ALL = ["store", "append", "load", "attn", "build", "select", "block", "qblock"]
 
 
 def _ok(S):
-    return dict(sh=S.make_shape(1, 4, 2, 64, 10, 10), q8=_quant(S), kv=S.PagedKV(16, 16, 16, None, None),
+    return dict(sh=S.make_shape(1, 4, 2, 64, 10, 10), q8=_quant(S), kv=S.PagedKV(32, 32, 16, None, None),
                 ix=S.BlockIndex(16, 16, 16, None), L=100)
 
 
@@ -70,7 +70,8 @@ def test_quant_cache_pointers_are_refused(S, field):
         a["q8"] = _quant(S, **{field: None})
         assert _calls(S, **a)[name]() == 1
         if field not in ("k_scale", "v_scale", "page_table"):
-            a["q8"] = _quant(S, **{field: 24})           # not 16-byte aligned
+            # pools 32-byte aligned, tails 16
+            a["q8"] = _quant(S, **{field: 16 if field.endswith("pool") else 24})
             assert _calls(S, **a)[name]() == 1
         a["q8"] = None
         assert _calls(S, **a)[name]() == 1
@@ -112,6 +113,7 @@ def test_formats_ranges_and_pointers_are_refused(S):
     assert _calls(S, K=2, ld=8, **a)["select"]() == 2    # fewer than the 3 always taken
     assert _calls(S, n_recent=0, **a)["select"]() == 2
     assert _calls(S, n_sink=-1, **a)["select"]() == 2
+    assert _calls(S, **{**a, "kv": S.PagedKV(32, 16, 16, None, None)})["block"]() == 1
     assert _calls(S, K=11, ld=11, **a)["block"]() == 2   # more entries than pages of a sequence
     assert S.lib().sfi_quant_poll_error(None, C.byref(C.c_int32())) == 1
     assert S.lib().sfi_block_workspace_size(C.byref(a["sh"]), None) == 1
