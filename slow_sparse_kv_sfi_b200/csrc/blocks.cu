@@ -125,74 +125,98 @@ __device__ __forceinline__ Where locate(const SelectArgs& a, int b, int len, int
   return w;
 }
 
-// Scores of a tile for KV head h, by one warp: lanes with t = 0 return block
-// tile * 16 + g, lanes with t = 1 block tile * 16 + 8 + g.
-template <int D, int NT>
-__device__ __forceinline__ float score_tile(const SelectArgs& a, int h, const Where& w, int lane,
-                                            const Query<D, NT>& s) {
+// Scores of U tiles for KV head h, by one warp, all loads first: u[i] of lanes
+// with t = 0 is that of block 16 * tile + g, of lanes with t = 1 that of block
+// 16 * tile + 8 + g.
+template <int D, int NT, int U>
+__device__ __forceinline__ void score_tiles(const SelectArgs& a, int h, const Where (&w)[U], int lane,
+                                            const Query<D, NT>& s, float (&u)[U]) {
   constexpr int KC = 2 * D / 64;
   const int t = lane & 3;
-  uint4 x[2][KC];
-  float sc[2];
+  uint4 x[U][2][KC];
+  float sc[U][2];
 #pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    sc[r] = 0.f;
+  for (int i = 0; i < U; ++i)
 #pragma unroll
-    for (int c = 0; c < KC; ++c) x[r][c] = make_uint4(0, 0, 0, 0);
-    if (w.page[r] < 0) continue;
-    const size_t ph = (size_t)w.page[r] * a.Hkv + h;
-    const uint4* row = reinterpret_cast<const uint4*>(a.bounds + ph * 2 * D);
+    for (int r = 0; r < 2; ++r) {
+      sc[i][r] = 0.f;
 #pragma unroll
-    for (int c = 0; c < KC; ++c) x[r][c] = __ldg(row + t + 4 * c);
-    sc[r] = __ldg(a.scale + ph);
-  }
-  float best[2] = {-INFINITY, -INFINITY};
+      for (int c = 0; c < KC; ++c) x[i][r][c] = make_uint4(0, 0, 0, 0);
+      if (w[i].page[r] < 0) continue;
+      const size_t ph = (size_t)w[i].page[r] * a.Hkv + h;
+      const uint4* row = reinterpret_cast<const uint4*>(a.bounds + ph * 2 * D);
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    int d[4] = {0, 0, 0, 0};
-#pragma unroll
-    for (int c = 0; c < KC; ++c) {
-      const uint4 q = s.b[nt][c][lane];
-      const uint32_t a0[4] = {x[0][c].x, x[1][c].x, x[0][c].y, x[1][c].y};
-      const uint32_t a1[4] = {x[0][c].z, x[1][c].z, x[0][c].w, x[1][c].w};
-      mma_s8_16832(d, a0, q.x, q.y);
-      mma_s8_16832(d, a1, q.z, q.w);
+      for (int c = 0; c < KC; ++c) x[i][r][c] = __ldg(row + t + 4 * c);
+      sc[i][r] = __ldg(a.scale + ph);
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int n = nt * 8 + 2 * t + (i & 1);
-      if (n < a.G) best[i >> 1] = fmaxf(best[i >> 1], (float)d[i] * s.e[n]);
+  for (int i = 0; i < U; ++i) {
+    float best[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      int d[4] = {0, 0, 0, 0};
+#pragma unroll
+      for (int c = 0; c < KC; ++c) {
+        const uint4 q = s.b[nt][c][lane];
+        const uint32_t a0[4] = {x[i][0][c].x, x[i][1][c].x, x[i][0][c].y, x[i][1][c].y};
+        const uint32_t a1[4] = {x[i][0][c].z, x[i][1][c].z, x[i][0][c].w, x[i][1][c].w};
+        mma_s8_16832(d, a0, q.x, q.y);
+        mma_s8_16832(d, a1, q.z, q.w);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int n = nt * 8 + 2 * t + (j & 1);
+        if (n < a.G) best[j >> 1] = fmaxf(best[j >> 1], (float)d[j] * s.e[n]);
+      }
+    }
+    const float big = __uint_as_float(0x7f7fffffu);
+    float v[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      best[r] = fmaxf(best[r], __shfl_xor_sync(0xffffffffu, best[r], 1));
+      best[r] = fmaxf(best[r], __shfl_xor_sync(0xffffffffu, best[r], 2));
+      v[r] = w[i].page[r] >= 0 ? fminf(fmaxf(best[r] * sc[i][r], -big), big) : w[i].fixed[r];
+    }
+    u[i] = t == 0 ? v[0] : v[1];
+  }
+}
+
+// Scores of the blocks below n of row (b, h), two tiles at a time, by warp
+// `first` of `warps`: put(block, score).
+template <int D, int NT, class Put>
+__device__ __forceinline__ void score_row(const SelectArgs& a, int b, int h, int len, int n, int first, int warps,
+                                          int lane, const Query<D, NT>& s, Put put) {
+  constexpr int U = 2;
+  Where w[U];
+#pragma unroll
+  for (int i = 0; i < U; ++i) w[i] = locate(a, b, len, first + i * warps, lane);
+  for (int tile = first; tile * 16 < n; tile += U * warps) {
+    Where next[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) next[i] = locate(a, b, len, tile + (U + i) * warps, lane);
+    float u[U];
+    score_tiles<D, NT, U>(a, h, w, lane, s, u);
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int j = (tile + i * warps) * 16 + (lane >> 2) + 8 * (lane & 1);
+      if ((lane & 2) == 0 && j < n) put(j, u[i]);
+      w[i] = next[i];
     }
   }
-  const float big = __uint_as_float(0x7f7fffffu);
-  float u[2];
-#pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    best[r] = fmaxf(best[r], __shfl_xor_sync(0xffffffffu, best[r], 1));
-    best[r] = fmaxf(best[r], __shfl_xor_sync(0xffffffffu, best[r], 2));
-    u[r] = w.page[r] >= 0 ? fminf(fmaxf(best[r] * sc[r], -big), big) : w.fixed[r];
-  }
-  return t == 0 ? u[0] : u[1];
 }
 
 // Scores alone, for rows that the select kernel does not hold.
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, 2) block_score_kernel(const SelectArgs a) {
+__global__ void __launch_bounds__(kThreads, 1) block_score_kernel(const SelectArgs a) {
   grid_dep_enter();
   __shared__ Query<D, NT> s;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int bh = blockIdx.y, b = bh / a.Hkv, h = bh - b * a.Hkv;
   load_query<D, NT>(a, b, h, s);
   const int len = seq_len(a.lens, a.L, b, a.err);
-  const int n_tiles = (a.nb + 15) / 16;
-  Where w = locate(a, b, len, blockIdx.x * kWarps + warp, lane);
-  for (int tile = blockIdx.x * kWarps + warp; tile < n_tiles; tile += gridDim.x * kWarps) {
-    const Where next = locate(a, b, len, tile + gridDim.x * kWarps, lane);
-    const float u = score_tile<D, NT>(a, h, w, lane, s);
-    w = next;
-    const int j = tile * 16 + (lane >> 2) + 8 * (lane & 1);
-    if ((lane & 2) == 0 && j < a.nb) a.scores[(size_t)bh * a.ld + j] = u;
-  }
+  float* row = a.scores + (size_t)bh * a.ld;
+  score_row<D, NT>(a, b, h, len, a.nb, blockIdx.x * kWarps + warp, gridDim.x * kWarps, lane, s,
+                   [&](int j, float u) { row[j] = u; });
 }
 
 // A key back to its score (the inverse of float_key).
@@ -205,7 +229,7 @@ constexpr int kBins = 4 * kThreads;
 
 struct Search {
   uint32_t cnt[2][kWarps][4];
-  int2 scan[kWarps];
+  int scan[kWarps];
   int hist[kBins];
   uint32_t cand[kThreads];
   int bin, above, m;
@@ -219,8 +243,10 @@ struct Search {
 // bisection over the keys: three thresholds a round, counted by the whole CTA.
 __device__ __forceinline__ uint32_t kth_key(const uint32_t* keys, int n, int K, Search& s) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // forced blocks, smallest and largest other key
+  // forced blocks, smallest and largest other key.  (Rolled loops over shared
+  // memory: this code runs once per CTA, so its own size costs most.)
   uint32_t mn = kForced, mx = 0u, forced = 0u;
+#pragma unroll 4
   for (int i = threadIdx.x; i < n; i += kThreads) {
     const uint32_t k = keys[i];
     forced += k == kForced;
@@ -251,15 +277,18 @@ __device__ __forceinline__ uint32_t kth_key(const uint32_t* keys, int n, int K, 
   const float s0 = fmaxf(key_score(lo), -3.402823466e38f);
   const float step = __fdiv_rn((float)kBins, key_score(hi) - s0);
   auto bin_of = [&](uint32_t k) { return max(0, min(kBins - 1, (int)((key_score(k) - s0) * step))); };
-  for (int i = threadIdx.x; i < n; i += kThreads)
-    if (keys[i] != kForced) atomicAdd(&s.hist[bin_of(keys[i])], 1);
+#pragma unroll 4
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    const uint32_t k = keys[i];
+    if (k != kForced) atomicAdd(&s.hist[bin_of(k)], 1);
+  }
   __syncthreads();
   // sums from the top: thread t owns bins kBins - 4 t - 1 down to kBins - 4 t - 4
-  int own[4], sum = 0;
+  int bins[4], sum = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    own[i] = s.hist[kBins - 1 - 4 * (int)threadIdx.x - i];
-    sum += own[i];
+    bins[i] = s.hist[kBins - 1 - 4 * (int)threadIdx.x - i];
+    sum += bins[i];
   }
   int x = sum;
 #pragma unroll
@@ -267,23 +296,24 @@ __device__ __forceinline__ uint32_t kth_key(const uint32_t* keys, int n, int K, 
     const int y = __shfl_up_sync(0xffffffffu, x, sh);
     if (lane >= sh) x += y;
   }
-  if (lane == 31) s.scan[warp].x = x;
+  if (lane == 31) s.scan[warp] = x;
   __syncthreads();
   int above = x - sum;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) above += w < warp ? s.scan[w].x : 0;
+  for (int w = 0; w < kWarps; ++w) above += w < warp ? s.scan[w] : 0;
   if (above < need && above + sum >= need) {   // one thread
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if (above < need && above + own[i] >= need) {
+      if (above < need && above + bins[i] >= need) {
         s.bin = kBins - 1 - 4 * (int)threadIdx.x - i;
         s.above = above;
       }
-      above += own[i];
+      above += bins[i];
     }
   }
   __syncthreads();
   const int bin = s.bin;
+#pragma unroll 4
   for (int i = threadIdx.x; i < n; i += kThreads) {
     const uint32_t k = keys[i];
     if (k != kForced && bin_of(k) == bin) {
@@ -313,6 +343,7 @@ __device__ __forceinline__ uint32_t kth_key(const uint32_t* keys, int n, int K, 
     // lo < m0 <= m1 <= m2 <= hi
     const uint32_t m0 = lo + (d >> 2) + 1, m1 = max(m0, lo + (d >> 1) + 1), m2 = max(m1, lo + (d >> 1) + (d >> 2) + 1);
     uint32_t c0 = 0, c1 = 0, c2 = 0;
+#pragma unroll 4
     for (int i = threadIdx.x; i < n; i += kThreads) {
       const uint32_t k = keys[i];
       c0 += k >= m0;
@@ -357,7 +388,7 @@ __device__ __forceinline__ uint32_t kth_key(const uint32_t* keys, int n, int K, 
 // share of the row's blocks into the first one's shared memory, which then
 // finds the K-th largest key and writes the chosen blocks in order.
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, 2) block_select_kernel(const SelectArgs a) {
+__global__ void __launch_bounds__(kThreads, 1) block_select_kernel(const SelectArgs a) {
   grid_dep_wait();
   namespace cg = cooperative_groups;
   cg::cluster_group cl = cg::this_cluster();
@@ -377,56 +408,53 @@ __global__ void __launch_bounds__(kThreads, 2) block_select_kernel(const SelectA
       for (int i = threadIdx.x; i < a.K; i += kThreads) out[i] = i;
     return;
   }
-  Where w = locate(a, b, len, rank * kWarps + warp, lane);
   load_query<D, NT>(a, b, h, sh.query);
   uint32_t* first = cl.map_shared_rank(keys, 0);
   cl.sync();   // the first CTA runs, so its shared memory may be written
-  for (int tile = rank * kWarps + warp; tile * 16 < n; tile += cs * kWarps) {
-    const Where next = locate(a, b, len, tile + cs * kWarps, lane);
-    const float u = score_tile<D, NT>(a, h, w, lane, sh.query);
-    w = next;
-    const int j = tile * 16 + (lane >> 2) + 8 * (lane & 1);
-    if ((lane & 2) == 0 && j < n) first[j] = u == INFINITY ? kForced : float_key(u);
-  }
+  score_row<D, NT>(a, b, h, len, n, rank * kWarps + warp, cs * kWarps, lane, sh.query,
+                   [&](int j, float u) { first[j] = u == INFINITY ? kForced : float_key(u); });
   cl.sync();
   if (rank != 0) return;
   const uint32_t lo = kth_key(keys, n, a.K, sh.search);
   __syncthreads();   // its shared memory is used again
-  int2* scan = sh.search.scan;
+  int* scan = sh.search.scan;
 
-  // All keys above lo, and the first of those equal to it.  Warp w takes the w-th run of positions,
-  // 32 at a time, so the chosen ones come out in order.
-  const int run = (n + 32 * kWarps - 1) / (32 * kWarps) * 32;
-  const int i0 = min(n, warp * run), i1 = min(n, i0 + run);
-  int above = 0, equal = 0;
-  for (int i = i0 + lane; i - lane < i1; i += 32) {
-    const uint32_t k = i < i1 ? keys[i] : 0u;
-    above += __popc(__ballot_sync(0xffffffffu, i < i1 && k > lo));
-    equal += __popc(__ballot_sync(0xffffffffu, i < i1 && k == lo));
+  // All keys above lo, and the first of those equal to it.  Warp w has the w-th
+  // run of positions, lane c the c-th 32 of it as two masks, so the chosen ones
+  // come out in order.
+  const int run = (n + 32 * kWarps - 1) / (32 * kWarps) * 32;   // at most 1024: 32 times 32
+  const int i0 = warp * run;
+  uint32_t ma = 0, me = 0;
+#pragma unroll 4
+  for (int c = 0; c < run / 32; ++c) {
+    const int i = i0 + c * 32 + lane;
+    const uint32_t k = i < n ? keys[i] : 0u;   // below lo
+    const uint32_t x = __ballot_sync(0xffffffffu, k > lo), y = __ballot_sync(0xffffffffu, k == lo);
+    if (lane == c) {
+      ma = x;
+      me = y;
+    }
   }
-  if (lane == 0) scan[warp] = make_int2(above, equal);
+  // both counts in one word: at most 16384 of each
+  const int own = __popc(ma) | (__popc(me) << 16);
+  int x = own;
+#pragma unroll
+  for (int sh_ = 1; sh_ < 32; sh_ <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, sh_);
+    if (lane >= sh_) x += y;
+  }
+  if (lane == 31) scan[warp] = x;
   __syncthreads();
-  int total = 0;
-  above = equal = 0;   // of the positions before this warp's run
+  int total = 0, before = x - own;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
-    const int2 v = scan[w];
-    total += v.x;
-    above += w < warp ? v.x : 0;
-    equal += w < warp ? v.y : 0;
+    total += scan[w] & 0xffff;
+    before += w < warp ? scan[w] : 0;
   }
-  const int take = a.K - total;   // how many of the equal ones
-  for (int i = i0 + lane; i - lane < i1; i += 32) {
-    const uint32_t k = i < i1 ? keys[i] : 0u;
-    const uint32_t below = (1u << lane) - 1u;
-    const uint32_t ma = __ballot_sync(0xffffffffu, i < i1 && k > lo);
-    const uint32_t me = __ballot_sync(0xffffffffu, i < i1 && k == lo);
-    const int eq = equal + __popc(me & below);
-    const bool chosen = (ma >> lane & 1u) || ((me >> lane & 1u) && eq < take);
-    if (chosen) out[above + __popc(ma & below) + min(eq, take)] = i;
-    above += __popc(ma);
-    equal += __popc(me);
-  }
+  const int take = a.K - total, eq = before >> 16;   // equal ones to take, and those in front of this lane's
+  int at = (before & 0xffff) + min(eq, take);
+  for (int drop = __popc(me) - max(take - eq, 0); drop > 0; --drop) me &= ~(0x80000000u >> __clz(me));
+  for (uint32_t m = ma | me; m; m &= m - 1) out[at++] = i0 + lane * 32 + __ffs(m) - 1;
 }
 
 template <int D, int NT>
@@ -533,10 +561,10 @@ sfi_status sfi_block_select(const sfi_shape* shape, const sfi_block_index* index
   const bool wide = a.G > 8;
   cudaError_t e;
   if (nb <= kMaxRow) {
-    // one launch: a cluster per row, as many CTAs as keep the GPU at two each
-    // multiprocessor and leave every warp a tile
+    // one launch: a cluster per row, as many CTAs as fit one each multiprocessor
+    // and leave every warp a tile
     int cs = 1;
-    while (cs < kMaxCluster && 2L * cs * BH <= 2L * num_sms() && cs * kWarps * 16 < nb) cs *= 2;
+    while (cs < kMaxCluster && 2L * cs * BH <= num_sms() && cs * kWarps * 16 < nb) cs *= 2;
     e = shape->D == 128 ? (wide ? launch_select<128, 2>(a, BH, cs, st) : launch_select<128, 1>(a, BH, cs, st))
                         : (wide ? launch_select<64, 2>(a, BH, cs, st) : launch_select<64, 1>(a, BH, cs, st));
   } else {
