@@ -80,6 +80,9 @@ struct PageAttnArgs {
 #ifndef PA_WB
 #define PA_WB 6
 #endif
+#ifndef PA_CT2
+#define PA_CT2 3
+#endif
 #ifndef PA_W2
 #define PA_W2 4
 #endif
@@ -115,8 +118,13 @@ struct Cfg {
   // registers hold one 4 KB tile in flight, less than the latency asks for);
   // none for bf16 pages, whose tile is twice as large.
   static constexpr int kAhead = FMT == kBf16 ? 0 : 1;
-  static constexpr int kCtas = NT == 2 ? 2 : PA_CT;                   // per SM
-  static constexpr int kSmem = W * NT * 8 * (D + 8) * 4 + W * NT * 8 * 2 * 4;   // merge of the warps
+  static constexpr int kCtas = NT == 2 ? PA_CT2 : PA_CT;                   // per SM
+  static constexpr int kMerge = W * NT * 8 * (D + 8) * 4 + W * NT * 8 * 2 * 4;   // merge of the warps
+  // Q fragments: registers, or (G > 8, whose accumulators take twice the
+  // registers) 16 bytes of shared memory per thread, column tile and two steps.
+  static constexpr bool kQShared = HM == kTwo;
+  static constexpr int kQ = kQShared ? W * NT * (D / 32) * 512 : 0;
+  static constexpr int kSmem = kMerge + kQ;
 };
 
 // The run of each CTA is `quota` tiles of the whole sequence.
@@ -437,21 +445,24 @@ __device__ __forceinline__ void attend_row(const PageAttnArgs& a, uint8_t* smem,
   // fragments (zero for heads past G).  8-bit pages: fp16, each head times the
   // power of two that takes its largest value into [2^14, 2^15) (an element
   // below 2^-39 of that loses bits); zq undoes it.
-  uint32_t qb[NT][D / 16][2];
+  constexpr int QN = C::kQShared ? 1 : NT;
+  uint32_t qb[QN][D / 16][2];
+  uint4* qs = reinterpret_cast<uint4*>(smem + C::kMerge) + warp * NT * (D / 32) * 32 + lane;
   float zq[NT][2];
   auto q_at = [&](int nt, int k) {   // four columns of the head of column nt * 8 + g
     const int n = HM == kHalf ? g & 3 : nt * 8 + g;
     if (n >= a.G) return make_uint2(0, 0);
     return __ldg(reinterpret_cast<const uint2*>(a.q + ((size_t)b * a.Hq + h * a.G + n) * D + C::k_col(t, k)));
   };
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
+  auto q_load = [&](int nt) {
 #pragma unroll
     for (int k = 0; k < D / 16; ++k) {
       const uint2 x = q_at(nt, k);
-      qb[nt][k][0] = x.x;
-      qb[nt][k][1] = x.y;
+      qb[nt % QN][k][0] = x.x;
+      qb[nt % QN][k][1] = x.y;
     }
+  };
+  if (!C::kQShared) q_load(0);   // ahead of the look-up; converted behind the first loads of K and V
 
   // Tiles of this warp: t0 + warp + W * i, i < n.  Lane l looks up tile i0 + l of
   // a batch of 32: block, page and scales.
@@ -563,8 +574,14 @@ __device__ __forceinline__ void attend_row(const PageAttnArgs& a, uint8_t* smem,
   }
 
   auto q_regs = [&](int nt, int k, uint32_t& b0, uint32_t& b1) {
-    b0 = qb[nt][k][0];
-    b1 = qb[nt][k][1];
+    if constexpr (C::kQShared) {
+      const uint4 x = qs[(nt * (D / 32) + k / 2) * 32];   // this thread's own words
+      b0 = k % 2 ? x.z : x.x;
+      b1 = k % 2 ? x.w : x.y;
+    } else {
+      b0 = qb[nt][k][0];
+      b1 = qb[nt][k][1];
+    }
   };
   Tile cur = tile_at(0);
   if (cur.page >= 0) {
@@ -573,13 +590,13 @@ __device__ __forceinline__ void attend_row(const PageAttnArgs& a, uint8_t* smem,
   }
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    uint32_t am = 0;
-#pragma unroll
-    for (int k = 0; k < D / 16; ++k) {
-      am = __vmaxu2(am, __vmaxu2(qb[nt][k][0] & 0x7fff7fffu, qb[nt][k][1] & 0x7fff7fffu));
-    }
+    uint32_t(&q)[D / 16][2] = qb[nt % QN];
+    if (C::kQShared) q_load(nt);
     zq[nt][0] = zq[nt][1] = a.scale_log2;
     if constexpr (FMT != kBf16) {
+      uint32_t am = 0;
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) am = __vmaxu2(am, __vmaxu2(q[k][0] & 0x7fff7fffu, q[k][1] & 0x7fff7fffu));
       am = max(am & 0xffffu, am >> 16);
       am = max(am, __shfl_xor_sync(0xffffffffu, am, 1));
       am = max(am, __shfl_xor_sync(0xffffffffu, am, 2));
@@ -591,14 +608,18 @@ __device__ __forceinline__ void attend_row(const PageAttnArgs& a, uint8_t* smem,
       for (int k = 0; k < D / 16; ++k)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const float2 x = unpack_bf16x2(qb[nt][k][i]);
-          qb[nt][k][i] = pack_f16x2(x.x * f, x.y * f);
+          const float2 x = unpack_bf16x2(q[k][i]);
+          q[k][i] = pack_f16x2(x.x * f, x.y * f);
         }
 #pragma unroll
       for (int j = 0; j < 2; ++j) zq[nt][j] *= __shfl_sync(0xffffffffu, inv, (2 * t + j) * 4);
     }
+    if constexpr (C::kQShared) {
+#pragma unroll
+      for (int k = 0; k < D / 16; k += 2)
+        qs[(nt * (D / 32) + k / 2) * 32] = make_uint4(q[k][0], q[k][1], q[k + 1][0], q[k + 1][1]);
+    }
   }
-
   for (int i = 0; i < n; ++i) {
     const Tile nxt = tile_at(i + 1);
     auto next_k = [&]() {
