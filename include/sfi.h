@@ -432,9 +432,12 @@ sfi_status sfi_quant_load(const sfi_shape* shape, const sfi_quant_kv* qkv, const
  *  q    bf16 [B, Hq, D], 16-byte aligned
  *  out  fp32 [B, Hq, D] = sum_j softmax(z)_j v_j, z_j = q.k_j / sqrt(D)
  *  lse  fp32 [B, Hq] natural-log sum of exp(z), or NULL
+ *       (out 16-byte aligned)
  * An empty sequence gets out = 0 and lse = -infinity.  ws: scratch of
- * sfi_block_workspace_size bytes, 16-byte aligned; it needs no clearing.
- * Calls that share one ws must not run concurrently. */
+ * sfi_block_workspace_size bytes, 16-byte aligned, zero-filled before its first
+ * use; every call leaves it ready for the next, of any of the four calls below
+ * and any lengths of the same shape.  Calls that share one ws must not run
+ * concurrently. */
 sfi_status sfi_quant_attn(const sfi_shape* shape, const sfi_quant_kv* qkv, int32_t L, const int32_t* lens,
                           const sfi_bf16* q, float* out, float* lse, void* ws, size_t ws_bytes,
                           sfi_stream stream);

@@ -503,6 +503,8 @@ BlockWs block_ws(const sfi_shape& s) {
   off += align_up(items * G * s.D * sizeof(float), 256);
   w.ml_off = off;
   off += align_up(items * G * 2 * sizeof(float), 256);
+  w.arrived_off = off;
+  off += align_up((size_t)BH * sizeof(int), 256);
   w.total = off;
   return w;
 }

@@ -199,9 +199,10 @@ int score_tile(int G);
 int stat_chunks(int nC);
 
 
-// Block-sparse and 8-bit calls: scratch is [scores][partials (O)][partials (m, l)].
+// Block-sparse and 8-bit calls: scratch is [scores][partials (O)][partials
+// (m, l)][arrival counts, zero between calls].
 struct BlockWs {
-  size_t score_off, part_off, ml_off, total;
+  size_t score_off, part_off, ml_off, arrived_off, total;
 };
 BlockWs block_ws(const sfi_shape& s);
 // CTAs of an attention launch over this many tiles, at most per_sm on each

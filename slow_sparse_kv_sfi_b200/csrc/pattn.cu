@@ -7,8 +7,9 @@
 // row being one (sequence, KV head), its tiles its pages or list entries - form
 // one sequence, and every CTA takes an equal run of it, whatever the lengths;
 // the grid is what the GPU holds at once.  A run cuts at most two rows: a row
-// inside one run is finished there, the pieces of the others are merged by a
-// second kernel.  Within a row, warp w of the CTA takes tiles w, w + W, ...;
+// inside one run is finished there, the pieces of the others are merged by the
+// CTA that writes the last of them (in the order of the pieces, whoever that
+// is).  Within a row, warp w of the CTA takes tiles w, w + W, ...;
 // each warp runs its own online softmax and the CTA merges its warps in shared
 // memory.
 //
@@ -62,12 +63,14 @@ struct PageAttnArgs {
   const int32_t* sel;               // LIST
   int64_t sel_ld;
   int K;
-  int ctas;                         // of the grid
+  int total;                        // tiles of all rows, or -1: by lens
+  int quota;                        // tiles of a CTA's run (total >= 0)
   float scale_log2;                 // log2(e) / sqrt(D)
   float* out;
   float* lse;
   float* part;                      // [cta][2][G][D]: piece of the row that began before, that goes on behind
   float* ml;                        // [cta][2][G][2]
+  int* arrived;                     // [B * Hkv] pieces of a row written so far; zero between calls
   int* err;
 };
 
@@ -127,63 +130,46 @@ struct Cfg {
   static constexpr int kSmem = kMerge + kQ;
 };
 
-// The run of each CTA is `quota` tiles of the whole sequence.
-constexpr int kMinQuota = PA_MINQ;   // a smaller run would not fill the warps of a CTA
-__host__ __device__ __forceinline__ long long quota(long long total, int ctas) {
-  const long long q = (total + ctas - 1) / ctas;
-  return q > kMinQuota ? q : kMinQuota;
-}
-
 // Tiles of a row of sequence b.
 template <bool LIST>
 __device__ __forceinline__ int row_tiles(const PageAttnArgs& a, int b, int* err) {
   return LIST ? a.K : (seq_len(a.lens, a.L, b, err) + kPage - 1) / kPage;
 }
 
-// Tiles of all rows, and of the rows of sequences before b (one warp; all
-// lanes get both).
-template <bool LIST>
-__device__ __forceinline__ void count_tiles(const PageAttnArgs& a, int b, int lane, int* err, long long& total,
-                                            long long& before) {
-  if (LIST || !a.lens) {
-    const long long per = (long long)row_tiles<LIST>(a, 0, err) * a.Hkv;
-    total = per * a.B;
-    before = per * b;
-    return;
-  }
-  long long t = 0, p = 0;
-  for (int i = lane; i < a.B; i += 32) {
-    const long long v = (long long)row_tiles<LIST>(a, i, err) * a.Hkv;
-    t += v;
-    if (i < b) p += v;
-  }
-#pragma unroll
-  for (int sh = 16; sh >= 1; sh >>= 1) {
-    t += __shfl_xor_sync(0xffffffffu, t, sh);
-    p += __shfl_xor_sync(0xffffffffu, p, sh);
-  }
-  total = t;
-  before = p;
+// The run of each CTA is `quota` tiles of the whole sequence of `total` tiles;
+// a smaller one than kMinQuota would not fill the warps of a CTA.
+constexpr int kMinQuota = PA_MINQ;
+__host__ __device__ __forceinline__ int quota(int total, int ctas) {
+  const int q = (int)(((unsigned)total + (unsigned)ctas - 1u) / (unsigned)ctas);
+  return q > kMinQuota ? q : kMinQuota;
+}
+
+// Tiles of all rows (one warp; all lanes get it).
+__device__ __forceinline__ int count_tiles(const PageAttnArgs& a, int lane, int* err) {
+  if (a.total >= 0) return a.total;   // rows of one length
+  int t = 0;
+  for (int i = lane; i < a.B; i += 32) t += row_tiles<false>(a, i, err);
+  return (int)__reduce_add_sync(0xffffffffu, (unsigned)t) * a.Hkv;
 }
 
 // The sequence whose rows hold tile `pos` (< total) and the first tile of its
 // rows (one warp; all lanes get both).
 template <bool LIST>
-__device__ __forceinline__ void find_sequence(const PageAttnArgs& a, long long pos, int lane, int& b, long long& first) {
-  if (LIST || !a.lens) {
-    const long long per = (long long)row_tiles<LIST>(a, 0, nullptr) * a.Hkv;
-    b = (int)(pos / per);
-    first = per * b;
+__device__ __forceinline__ void find_sequence(const PageAttnArgs& a, int pos, int lane, int& b, int& first) {
+  if (a.total >= 0) {
+    const unsigned per = (unsigned)a.total / (unsigned)a.B;
+    b = (int)((unsigned)pos / per);
+    first = (int)per * b;
     return;
   }
-  long long base = 0;
+  int base = 0;
   for (int i0 = 0; i0 < a.B; i0 += 32) {
     const int i = i0 + lane;
-    const long long v = i < a.B ? (long long)row_tiles<LIST>(a, i, nullptr) * a.Hkv : 0;
-    long long x = v;
+    const int v = i < a.B ? row_tiles<LIST>(a, i, nullptr) * a.Hkv : 0;
+    int x = v;
 #pragma unroll
     for (int sh = 1; sh < 32; sh <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, x, sh);
+      const int y = __shfl_up_sync(0xffffffffu, x, sh);
       if (lane >= sh) x += y;
     }
     const unsigned hit = __ballot_sync(0xffffffffu, base + x > pos);
@@ -429,11 +415,31 @@ __device__ __forceinline__ void tile_math(State<D, NT>& st, const float (&zf)[NT
   }
 }
 
+__device__ __forceinline__ void add_scaled(float4& o, float f, const float4& x) {
+  o.x = fmaf(f, x.x, o.x);
+  o.y = fmaf(f, x.y, o.y);
+  o.z = fmaf(f, x.z, o.z);
+  o.w = fmaf(f, x.w, o.w);
+}
+
+// Columns d .. d + 3 of an output row (and its log-sum-exp) from (m, l, O);
+// l = 0: nothing to attend to.
+template <int D>
+__device__ __forceinline__ void write_out(const PageAttnArgs& a, size_t row, int d, float M, float l, const float4& o) {
+  const bool none = l == 0.f;
+  const float r = none ? 0.f : __fdiv_rn(1.f, l);
+  *reinterpret_cast<float4*>(a.out + row * D + d) = make_float4(o.x * r, o.y * r, o.z * r, o.w * r);
+  if (d == 0 && a.lse) a.lse[row] = none ? -INFINITY : (M + fast_log2(l)) * kLn2;
+}
+
+constexpr int kMaxGroups = 8;
+
 // Tiles [t0, t1) of the T tiles of row (b, h), by the whole CTA: the row's
-// output, or (not the whole row) its piece for the merge.
+// output, or (not the whole row) its piece, and the output too if that is the
+// last.  row0: the row's first tile among all.
 template <int D, int FMT, int HM, bool LIST>
 __device__ __forceinline__ void attend_row(const PageAttnArgs& a, uint8_t* smem, int b, int h, int len, int T, int t0,
-                                           int t1) {
+                                           int t1, int row0, int quota_) {
   using C = Cfg<D, FMT, HM>;
   constexpr int NT = C::NT, W = C::W, KJ = C::KJ, VC = C::VC;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -445,8 +451,7 @@ __device__ __forceinline__ void attend_row(const PageAttnArgs& a, uint8_t* smem,
   // fragments (zero for heads past G).  8-bit pages: fp16, each head times the
   // power of two that takes its largest value into [2^14, 2^15) (an element
   // below 2^-39 of that loses bits); zq undoes it.
-  constexpr int QN = C::kQShared ? 1 : NT;
-  uint32_t qb[QN][D / 16][2];
+  uint32_t qb[NT][D / 16][2];
   uint4* qs = reinterpret_cast<uint4*>(smem + C::kMerge) + warp * NT * (D / 32) * 32 + lane;
   float zq[NT][2];
   auto q_at = [&](int nt, int k) {   // four columns of the head of column nt * 8 + g
@@ -454,15 +459,15 @@ __device__ __forceinline__ void attend_row(const PageAttnArgs& a, uint8_t* smem,
     if (n >= a.G) return make_uint2(0, 0);
     return __ldg(reinterpret_cast<const uint2*>(a.q + ((size_t)b * a.Hq + h * a.G + n) * D + C::k_col(t, k)));
   };
-  auto q_load = [&](int nt) {
+  // ahead of the look-up; converted behind the first loads of K and V
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int k = 0; k < D / 16; ++k) {
       const uint2 x = q_at(nt, k);
-      qb[nt % QN][k][0] = x.x;
-      qb[nt % QN][k][1] = x.y;
+      qb[nt][k][0] = x.x;
+      qb[nt][k][1] = x.y;
     }
-  };
-  if (!C::kQShared) q_load(0);   // ahead of the look-up; converted behind the first loads of K and V
 
   // Tiles of this warp: t0 + warp + W * i, i < n.  Lane l looks up tile i0 + l of
   // a batch of 32: block, page and scales.
@@ -471,28 +476,36 @@ __device__ __forceinline__ void attend_row(const PageAttnArgs& a, uint8_t* smem,
   auto look_up = [&](int i0) {
     mine = Tile{-1, 0, 0.f, 0.f};
     const int i = i0 + lane;
-    if (i >= n) return;
     const int tile = t0 + warp + W * i;
-    const int blk = LIST ? __ldg(a.sel + (size_t)bh * a.sel_ld + tile) : tile;
-    if ((unsigned)blk >= (unsigned)blocks) return;
-    mine.rows = min(kPage, len - blk * kPage);
-    if (FMT != kBf16 && mine.rows < kPage) {
-      mine.page = -2;
-      return;
+    const int blk = i >= n ? -1 : LIST ? __ldg(a.sel + (size_t)bh * a.sel_ld + tile) : tile;
+    if ((unsigned)blk < (unsigned)blocks) {
+      mine.rows = min(kPage, len - blk * kPage);
+      if (FMT != kBf16 && mine.rows < kPage) {
+        mine.page = -2;
+      } else {
+        const int page = __ldg(a.pt + (size_t)b * a.max_pages + blk);
+        if ((unsigned)page < (unsigned)a.num_pages) {
+          mine.page = page;
+          if (FMT != kBf16) {
+            mine.ks = __ldg(a.ks + (size_t)page * a.Hkv + h);
+            mine.vs = __ldg(a.vs + (size_t)page * a.Hkv + h);
+          }
+        } else {
+          latch_error(a.err, SFI_ERR_DEVICE_CHECK, kSitePageAttn);
+          mine.rows = 0;
+        }
+      }
     }
-    const int page = __ldg(a.pt + (size_t)b * a.max_pages + blk);
-    if ((unsigned)page >= (unsigned)a.num_pages) {
-      latch_error(a.err, SFI_ERR_DEVICE_CHECK, kSitePageAttn);
-      mine.rows = 0;
-      return;
-    }
-    mine.page = page;
-    if (FMT != kBf16) {
-      mine.ks = __ldg(a.ks + (size_t)page * a.Hkv + h);
-      mine.vs = __ldg(a.vs + (size_t)page * a.Hkv + h);
+    // the tail's rows are not loaded ahead of their use: bring them close
+    if (FMT != kBf16 && __any_sync(0xffffffffu, mine.page == -2)) {
+      const char* kt = reinterpret_cast<const char*>(a.k_tail + (size_t)bh * (kPage * D));
+      const char* vt = reinterpret_cast<const char*>(a.v_tail + (size_t)bh * (kPage * D));
+      for (int o = lane * 128; o < kPage * D * 2; o += 32 * 128) {
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(kt + o));
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(vt + o));
+      }
     }
   };
-
   // The warp brings a tile into L2 kAhead tiles before it loads it.
   auto fetch = [&](int j) {
     const int page = __shfl_sync(0xffffffffu, mine.page, j);
@@ -590,8 +603,7 @@ __device__ __forceinline__ void attend_row(const PageAttnArgs& a, uint8_t* smem,
   }
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    uint32_t(&q)[D / 16][2] = qb[nt % QN];
-    if (C::kQShared) q_load(nt);
+    uint32_t(&q)[D / 16][2] = qb[nt];
     zq[nt][0] = zq[nt][1] = a.scale_log2;
     if constexpr (FMT != kBf16) {
       uint32_t am = 0;
@@ -747,26 +759,82 @@ __device__ __forceinline__ void attend_row(const PageAttnArgs& a, uint8_t* smem,
   __syncthreads();
   const bool whole = t0 == 0 && t1 == T;
   const int item = blockIdx.x * 2 + (t0 > 0 ? 0 : 1);
-  for (int e = threadIdx.x; e < a.G * D; e += W * 32) {
-    const int n_ = e / D, d = e - n_ * D;
+  for (int e = threadIdx.x; e < a.G * (D / 4); e += W * 32) {
+    const int n_ = e / (D / 4), d = e % (D / 4) * 4;
     float M = kNoMax;
 #pragma unroll
     for (int w = 0; w < W; ++w) M = fmaxf(M, sml[(w * NT * 8 + n_) * 2]);
-    float l = 0.f, o = 0.f;
+    float l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < W; ++w) {
-      const float f = fast_exp2(sml[(w * NT * 8 + n_) * 2] - M);
-      l += f * sml[(w * NT * 8 + n_) * 2 + 1];
-      o += f * (so[(size_t)(w * NT * 8 + n_) * kLd + d] + (HM == kHalf ? so[(size_t)(w * 8 + n_ + 4) * kLd + d] : 0.f));
+      const float2 ml = *reinterpret_cast<const float2*>(sml + (w * NT * 8 + n_) * 2);
+      const float f = fast_exp2(ml.x - M);
+      l += f * ml.y;
+      add_scaled(o, f, *reinterpret_cast<const float4*>(so + (w * NT * 8 + n_) * kLd + d));
+      if (HM == kHalf) add_scaled(o, f, *reinterpret_cast<const float4*>(so + (w * 8 + n_ + 4) * kLd + d));
     }
     if (whole) {
-      const size_t row = (size_t)b * a.Hq + h * a.G + n_;
-      a.out[row * D + d] = l == 0.f ? 0.f : o / l;
-      if (d == 0 && a.lse) a.lse[row] = l == 0.f ? -INFINITY : (M + fast_log2(l)) * kLn2;
+      write_out<D>(a, (size_t)b * a.Hq + h * a.G + n_, d, M, l, o);
     } else {
-      a.part[((size_t)item * a.G + n_) * D + d] = o;
+      *reinterpret_cast<float4*>(a.part + ((size_t)item * a.G + n_) * D + d) = o;
       if (d == 0) *reinterpret_cast<float2*>(a.ml + ((size_t)item * a.G + n_) * 2) = make_float2(M, l);
     }
+  }
+  if (whole) return;
+
+  // The CTA that writes a row's last piece merges them all.
+  const int c0 = (int)((unsigned)row0 / (unsigned)quota_), c1 = (int)((unsigned)(row0 + T - 1) / (unsigned)quota_);
+  __syncthreads();   // the piece is written
+  int* last = reinterpret_cast<int*>(sml);   // the warps' (m, l) are used up
+  if (threadIdx.x == 0) {
+    __threadfence();   // the CTA's piece before the count
+    const bool all = atomicAdd(a.arrived + bh, 1) == c1 - c0;
+    __threadfence();   // the count before the others' pieces
+    if (all) a.arrived[bh] = 0;   // for the next call
+    *last = all;
+  }
+  __syncthreads();
+  if (!*last) return;
+  // slots of 4 columns; threads beyond them share the pieces out in groups
+  const int slots = a.G * (D / 4), groups = max(1, min(W * 32 / slots, kMaxGroups));
+  for (int e = threadIdx.x; e < slots * groups; e += W * 32) {
+    const int grp = e / slots, slot = e % slots, n_ = slot / (D / 4), d = slot % (D / 4) * 4;
+    float M = kNoMax, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int c = c0 + grp; c <= c1; c += groups) {
+      const size_t r = ((size_t)c * 2 + (c > c0 ? 0 : 1)) * a.G + n_;   // only the first piece begins inside its run
+      const float2 ml = __ldcg(reinterpret_cast<const float2*>(a.ml + r * 2));
+      const float4 x = __ldcg(reinterpret_cast<const float4*>(a.part + r * D + d));
+      const float mn = fmaxf(M, ml.x);
+      const float f0 = fast_exp2(M - mn), f1 = fast_exp2(ml.x - mn);
+      l = l * f0 + ml.y * f1;
+      o = make_float4(o.x * f0, o.y * f0, o.z * f0, o.w * f0);
+      add_scaled(o, f1, x);
+      M = mn;
+    }
+    if (groups == 1) {
+      write_out<D>(a, (size_t)b * a.Hq + h * a.G + n_, d, M, l, o);
+    } else {   // one pass of the loop: slots * groups <= threads
+      float* g_ = so + e * 8;
+      *reinterpret_cast<float4*>(g_) = o;
+      *reinterpret_cast<float2*>(g_ + 4) = make_float2(M, l);
+    }
+  }
+  if (groups == 1) return;
+  __syncthreads();
+  for (int slot = threadIdx.x; slot < slots; slot += W * 32) {
+    float M = kNoMax, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < groups; ++i) M = fmaxf(M, so[(i * slots + slot) * 8 + 4]);
+    for (int i = 0; i < groups; ++i) {
+      const float* g_ = so + (i * slots + slot) * 8;
+      const float f = fast_exp2(g_[4] - M);
+      l += f * g_[5];
+      add_scaled(o, f, *reinterpret_cast<const float4*>(g_));
+    }
+    write_out<D>(a, (size_t)b * a.Hq + h * a.G + slot / (D / 4), slot % (D / 4) * 4, M, l, o);
   }
 }
 
@@ -776,20 +844,19 @@ __global__ void __launch_bounds__(Cfg<D, FMT, HM>::W * 32, Cfg<D, FMT, HM>::kCta
   extern __shared__ __align__(16) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   grid_dep_wait();
-  grid_dep_launch();
-
-  // this CTA's run: `left` tiles from tile t0 of row (b, h) on
-  int b, h, t0, left;
-  {
-    long long total, unused, first;
-    count_tiles<LIST>(a, 0, lane, warp == 0 ? a.err : nullptr, total, unused);
-    const long long q = quota(total, a.ctas), pos = q * blockIdx.x;
-    if (pos >= total) return;
-    left = (int)min(q, total - pos);
+  // this CTA's run: `left` tiles from tile t0 of row (b, h) on, whose first tile is row0
+  const int total = count_tiles(a, lane, warp == 0 ? a.err : nullptr);
+  const int run = a.total >= 0 ? a.quota : quota(total, gridDim.x);
+  int b, h, t0, row0;
+  const int pos = (int)min((long long)run * blockIdx.x, (long long)total);
+  int left = min(run, total - pos);
+  if (left > 0) {
+    int first;
     find_sequence<LIST>(a, pos, lane, b, first);
     const int T = row_tiles<LIST>(a, b, nullptr);
-    h = (int)((pos - first) / T);
-    t0 = (int)(pos - first - (long long)h * T);
+    h = (int)((unsigned)(pos - first) / (unsigned)T);
+    row0 = first + h * T;
+    t0 = pos - row0;
   }
   for (; left > 0; ++b, h = 0) {   // sequences
     const int len = seq_len(a.lens, a.L, b, nullptr);
@@ -797,70 +864,20 @@ __global__ void __launch_bounds__(Cfg<D, FMT, HM>::W * 32, Cfg<D, FMT, HM>::kCta
     if (T == 0) continue;
     for (; h < a.Hkv && left > 0; ++h) {   // rows
       const int t1 = min(T, t0 + left);
-      attend_row<D, FMT, HM, LIST>(a, smem, b, h, len, T, t0, t1);
+      attend_row<D, FMT, HM, LIST>(a, smem, b, h, len, T, t0, t1, row0, run);
       left -= t1 - t0;
+      row0 += T;
       t0 = 0;
       __syncthreads();   // the row's shared memory is free
     }
   }
-}
-
-// Merge of the pieces of a row for one query head: the CTAs whose runs the row
-// spans, D threads a piece, kGroups pieces at once.  Rows that one CTA finished
-// are passed over; rows without tiles get their empty result here.
-constexpr int kGroups = 4;
-template <int D, bool LIST>
-__global__ void __launch_bounds__(kGroups * D) page_merge_kernel(const __grid_constant__ PageAttnArgs a) {
-  grid_dep_wait();
-  __shared__ float so[kGroups][D], sl[kGroups], sm[kGroups];
-  const int row = blockIdx.x, b = row / a.Hq, hq = row - b * a.Hq;
-  const int h = hq / a.G, n_ = hq - h * a.G;
-  const int grp = threadIdx.x / D, d = threadIdx.x % D;
-  long long total, first;
-  count_tiles<LIST>(a, b, threadIdx.x & 31, nullptr, total, first);
-  const int T = row_tiles<LIST>(a, b, nullptr);
-  if (T == 0) {
-    if (grp == 0) {
-      a.out[(size_t)row * D + d] = 0.f;
-      if (d == 0 && a.lse) a.lse[row] = -INFINITY;
+  if (a.total < 0) {   // the outputs of empty sequences
+    for (int i = blockIdx.x; i < a.B; i += gridDim.x) {
+      if (row_tiles<LIST>(a, i, nullptr) > 0) continue;
+      for (int e = threadIdx.x; e < a.Hq * (D / 4); e += blockDim.x)
+        write_out<D>(a, (size_t)i * a.Hq + e / (D / 4), e % (D / 4) * 4, 0.f, 0.f, make_float4(0.f, 0.f, 0.f, 0.f));
     }
-    return;
   }
-  first += (long long)h * T;
-  const long long q = quota(total, a.ctas);
-  const int c0 = (int)(first / q), c1 = (int)((first + T - 1) / q);
-  if (c0 == c1) return;
-  float M = kNoMax, l = 0.f, o = 0.f;
-#pragma unroll 4
-  for (int c = c0 + grp; c <= c1; c += kGroups) {
-    const size_t r = ((size_t)c * 2 + (c > c0 ? 0 : 1)) * a.G + n_;   // only the first piece begins inside its run
-    const float2 ml = __ldg(reinterpret_cast<const float2*>(a.ml + r * 2));
-    const float x = __ldg(a.part + r * D + d);
-    const float mn = fmaxf(M, ml.x);
-    const float f0 = fast_exp2(M - mn), f1 = fast_exp2(ml.x - mn);
-    l = l * f0 + ml.y * f1;
-    o = o * f0 + x * f1;
-    M = mn;
-  }
-  so[grp][d] = o;
-  if (d == 0) {
-    sl[grp] = l;
-    sm[grp] = M;
-  }
-  __syncthreads();
-  if (grp != 0) return;
-  M = kNoMax;
-#pragma unroll
-  for (int i = 0; i < kGroups; ++i) M = fmaxf(M, sm[i]);
-  l = o = 0.f;
-#pragma unroll
-  for (int i = 0; i < kGroups; ++i) {
-    const float f = fast_exp2(sm[i] - M);
-    l += f * sl[i];
-    o += f * so[i][d];
-  }
-  a.out[(size_t)row * D + d] = l == 0.f ? 0.f : o / l;
-  if (d == 0 && a.lse) a.lse[row] = l == 0.f ? -INFINITY : (M + fast_log2(l)) * kLn2;
 }
 
 #define SFI_TRY(x)               \
@@ -886,13 +903,11 @@ sfi_status launch(PageAttnArgs& a, cudaStream_t st) {
   }
   const int T = LIST ? a.K : (a.L + kPage - 1) / kPage;
   const long long total = (long long)a.B * a.Hkv * T;
-  a.ctas = page_attn_ctas(total, C::kCtas);
-  if (quota(total, a.ctas) > 0x7fffffffLL) return SFI_ERR_SHAPE;
-  const sfi_status r = cuda_status(launch_k(k, dim3(a.ctas), dim3(C::W * 32), C::kSmem, st, a));
-  // no row is cut when every run is a whole number of rows of one length
-  const bool cut = (!LIST && a.lens) || quota(total, a.ctas) % T != 0;
-  if (r != SFI_OK || !cut) return r;
-  return cuda_status(launch_k(page_merge_kernel<D, LIST>, dim3(a.B * a.Hq), dim3(kGroups * D), 0, st, a));
+  if (total > 0x7fffffffLL) return SFI_ERR_SHAPE;
+  const int ctas = page_attn_ctas(total, C::kCtas);
+  a.total = !LIST && a.lens ? -1 : (int)total;
+  a.quota = quota((int)total, ctas);
+  return cuda_status(launch_k(k, dim3(ctas), dim3(C::W * 32), C::kSmem, st, a));
 }
 
 template <int D, int FMT, bool LIST>
@@ -914,7 +929,7 @@ sfi_status run(const sfi_shape* shape, const sfi_paged_kv* kv, const sfi_quant_k
   SFI_TRY(check_shape(shape));
   SFI_TRY(q8 ? check_quant(q8) : check_kv(kv));
   SFI_TRY(check_L(shape, L));
-  if (!q || !aligned16(q) || !out) return SFI_ERR_INVALID_ARG;
+  if (!q || !aligned16(q) || !out || !aligned16(out)) return SFI_ERR_INVALID_ARG;
   // the kernel loads the pools 32 bytes at a time
   const uintptr_t pools = q8 ? reinterpret_cast<uintptr_t>(q8->k_pool) | reinterpret_cast<uintptr_t>(q8->v_pool)
                              : reinterpret_cast<uintptr_t>(kv->k_pool) | reinterpret_cast<uintptr_t>(kv->v_pool);
@@ -961,6 +976,7 @@ sfi_status run(const sfi_shape* shape, const sfi_paged_kv* kv, const sfi_quant_k
   a.lse = lse;
   a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + w.part_off);
   a.ml = reinterpret_cast<float*>(static_cast<char*>(ws) + w.ml_off);
+  a.arrived = reinterpret_cast<int*>(static_cast<char*>(ws) + w.arrived_off);
   cudaStream_t st = (cudaStream_t)stream;
   const int D = shape->D;
   if (!q8) return launch_any<kBf16, true>(D, a, st);

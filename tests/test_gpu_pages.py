@@ -69,7 +69,7 @@ class Case:
         self.q8 = S.make_quant_kv(self.kc, self.vc, self.ks, self.vs, self.ktail, self.vtail, self.ptd,
                                   _fmt(self.fmt), self.err)
         self.ix = S.make_block_index(self.bounds, self.bscale, self.ptd, self.err)
-        self.ws = torch.full((S.sfi_block_workspace_size(self.shape),), 0xA5, dtype=torch.uint8, device=DEV)
+        self.ws = torch.zeros(S.sfi_block_workspace_size(self.shape), dtype=torch.uint8, device=DEV)
         self.out = torch.full((B, self.Hq, D), float("nan"), device=DEV)
         self.lse = torch.full((B, self.Hq), float("nan"), device=DEV)
         return self
