@@ -389,7 +389,7 @@ __device__ __forceinline__ uint32_t kth_key(const uint32_t* keys, int n, int K, 
 // finds the K-th largest key and writes the chosen blocks in order.
 template <int D, int NT>
 __global__ void __launch_bounds__(kThreads, 1) block_select_kernel(const SelectArgs a) {
-  grid_dep_wait();
+  grid_dep_enter();
   namespace cg = cooperative_groups;
   cg::cluster_group cl = cg::this_cluster();
   extern __shared__ __align__(16) uint32_t keys[];   // of the cluster's first CTA

@@ -843,7 +843,7 @@ __global__ void __launch_bounds__(Cfg<D, FMT, HM>::W * 32, Cfg<D, FMT, HM>::kCta
     page_attn_kernel(const __grid_constant__ PageAttnArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  grid_dep_wait();
+  grid_dep_enter();   // the next launch may come up while this one runs; it waits before it touches memory
   // this CTA's run: `left` tiles from tile t0 of row (b, h) on, whose first tile is row0
   const int total = count_tiles(a, lane, warp == 0 ? a.err : nullptr);
   const int run = a.total >= 0 ? a.quota : quota(total, gridDim.x);
