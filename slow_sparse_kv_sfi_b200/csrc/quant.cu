@@ -68,24 +68,63 @@ __device__ __forceinline__ float tame(float x) {
   return x != x ? 0.f : fminf(fmaxf(x, -big), big);
 }
 
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {   // bf16 pairs; NaN stays
+  const __nv_bfloat162 r = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 r = __hmin2_nan(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// What a page's codes and bounds go by: its largest magnitude (bf16 bits; 0x7f80
+// and above: not finite) and, for keys, each dimension's extremes (this lane's
+// 8 values, the same in the lanes of other rows).
+struct Extremes {
+  uint32_t amax;
+  uint32_t hi[4], lo[4];
+};
+template <int D, bool KEYS>
+__device__ __forceinline__ Extremes extremes(const uint4 (&x)[Lay<D>::NI]) {
+  using Y = Lay<D>;
+  Extremes e;
+  uint32_t m = 0;
+  if constexpr (KEYS) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      e.hi[j] = e.lo[j] = j == 0 ? x[0].x : j == 1 ? x[0].y : j == 2 ? x[0].z : x[0].w;
+#pragma unroll
+      for (int i = 1; i < Y::NI; ++i) {
+        const uint32_t w = j == 0 ? x[i].x : j == 1 ? x[i].y : j == 2 ? x[i].z : x[i].w;
+        e.hi[j] = max2(e.hi[j], w);
+        e.lo[j] = min2(e.lo[j], w);
+      }
+#pragma unroll
+      for (int sh = Y::CH; sh < 32; sh <<= 1) {
+        e.hi[j] = max2(e.hi[j], __shfl_xor_sync(0xffffffffu, e.hi[j], sh));
+        e.lo[j] = min2(e.lo[j], __shfl_xor_sync(0xffffffffu, e.lo[j], sh));
+      }
+      m = __vmaxu2(m, __vmaxu2(e.hi[j] & 0x7fff7fffu, e.lo[j] & 0x7fff7fffu));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < Y::NI; ++i)
+      m = __vmaxu2(m, __vmaxu2(__vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu),
+                               __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu)));
+  }
+  e.amax = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
+  return e;
+}
+
 // Codes and scale of the page in x (this lane's 8 values of NI rows).
 template <int D, int FMT>
-__device__ __forceinline__ void write_codes(const uint4 (&x)[Lay<D>::NI], int lane, uint8_t* codes, float* scale) {
+__device__ __forceinline__ void write_codes(const uint4 (&x)[Lay<D>::NI], uint32_t amax_bits, int lane, uint8_t* codes,
+                                            float* scale) {
   using Y = Lay<D>;
-  uint32_t amax2 = 0;   // bf16x2 magnitudes compare as integers; NaN and infinity are the largest
-#pragma unroll
-  for (int i = 0; i < Y::NI; ++i) {
-    const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) amax2 = __vmaxu2(amax2, w[j] & 0x7fff7fffu);
-  }
-  uint32_t am = max(amax2 & 0xffffu, amax2 >> 16);
-#pragma unroll
-  for (int sh = 16; sh >= 1; sh >>= 1) am = max(am, __shfl_xor_sync(0xffffffffu, am, sh));
-  const bool finite = am < 0x7f80u;
-  const float amax = fmaxf(__uint_as_float(am << 16), kAmaxFloor);
+  const bool finite = amax_bits < 0x7f80u;
+  const float amax = fmaxf(__uint_as_float(amax_bits << 16), kAmaxFloor);
   constexpr float Q = FMT == SFI_FMT_E4M3 ? 448.f : 127.f;
-  const float inv = __fdiv_rn(Q, amax);
+  const float inv = finite ? __fdiv_rn(Q, amax) : 0.f;
   if (lane == 0) *scale = finite ? __fdiv_rn(amax, Q) : __uint_as_float(0x7fc00000u);
   const int row0 = lane / Y::CH, ch = lane % Y::CH;
 #pragma unroll
@@ -95,57 +134,75 @@ __device__ __forceinline__ void write_codes(const uint4 (&x)[Lay<D>::NI], int la
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const float2 a = bf2(w[2 * j]), b = bf2(w[2 * j + 1]);
-      uint32_t r;
       if constexpr (FMT == SFI_FMT_E4M3) {
         const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a.x * inv, a.y * inv), __NV_SATFINITE, __NV_E4M3);
         const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(b.x * inv, b.y * inv), __NV_SATFINITE, __NV_E4M3);
-        r = lo | (hi << 16);
+        o[j] = lo | (hi << 16);
       } else {
-        const int c0 = __float2int_rn(a.x * inv), c1 = __float2int_rn(a.y * inv);
-        const int c2 = __float2int_rn(b.x * inv), c3 = __float2int_rn(b.y * inv);
-        r = (c0 & 255) | ((c1 & 255) << 8) | ((c2 & 255) << 16) | ((uint32_t)(c3 & 255) << 24);
+        // the low byte of 1.5 * 2^23 + y is y rounded to an integer, ties to
+        // even (the product is rounded first, as the definition has it)
+        const float big = 12582912.f;
+        const uint32_t c0 = __float_as_uint(__fadd_rn(__fmul_rn(a.x, inv), big));
+        const uint32_t c1 = __float_as_uint(__fadd_rn(__fmul_rn(a.y, inv), big));
+        const uint32_t c2 = __float_as_uint(__fadd_rn(__fmul_rn(b.x, inv), big));
+        const uint32_t c3 = __float_as_uint(__fadd_rn(__fmul_rn(b.y, inv), big));
+        o[j] = __byte_perm(__byte_perm(c0, c1, 0x0040), __byte_perm(c2, c3, 0x0040), 0x5410);
       }
-      o[j] = finite ? r : 0u;
+      if (!finite) o[j] = 0u;   // infinity * 0 is not
     }
     *reinterpret_cast<uint2*>(codes + (size_t)(i * Y::RPI + row0) * D + ch * 8) = make_uint2(o[0], o[1]);
   }
 }
 
-// Bounds of the page in x: per dimension the largest and smallest key, over
-// the page's power-of-two scale, rounded outwards.
+// Bounds of a page of keys: per dimension the largest and smallest, over the
+// page's power-of-two scale, rounded outwards.
 template <int D>
-__device__ __forceinline__ void write_bounds(const uint4 (&x)[Lay<D>::NI], int lane, int8_t* bounds, float* scale) {
+__device__ __forceinline__ void write_bounds(const uint4 (&x)[Lay<D>::NI], const Extremes& ex, int lane, int8_t* bounds,
+                                             float* scale) {
   using Y = Lay<D>;
   float hi[8], lo[8];
+  float amax = __uint_as_float(ex.amax << 16);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    hi[e] = -INFINITY;
-    lo[e] = INFINITY;
+  for (int j = 0; j < 4; ++j) {
+    const float2 a = bf2(ex.hi[j]), b = bf2(ex.lo[j]);
+    hi[2 * j] = a.x;
+    hi[2 * j + 1] = a.y;
+    lo[2 * j] = b.x;
+    lo[2 * j + 1] = b.y;
   }
+  if (ex.amax >= 0x7f80u) {   // not finite: again, with the values that count
 #pragma unroll
-  for (int i = 0; i < Y::NI; ++i) {
-    const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 a = bf2(w[j]);
-      const float u = tame(a.x), v = tame(a.y);
-      hi[2 * j] = fmaxf(hi[2 * j], u);
-      lo[2 * j] = fminf(lo[2 * j], u);
-      hi[2 * j + 1] = fmaxf(hi[2 * j + 1], v);
-      lo[2 * j + 1] = fminf(lo[2 * j + 1], v);
+    for (int e = 0; e < 8; ++e) {
+      hi[e] = -INFINITY;
+      lo[e] = INFINITY;
     }
-  }
-  float amax = 0.f;
+#pragma unroll 1
+    for (int i = 0; i < Y::NI; ++i) {
+      uint4 v = x[0];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
+      for (int k = 1; k < Y::NI; ++k)
+        if (k == i) v = x[k];
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int sh = Y::CH; sh < 32; sh <<= 1) {
-      hi[e] = fmaxf(hi[e], __shfl_xor_sync(0xffffffffu, hi[e], sh));
-      lo[e] = fminf(lo[e], __shfl_xor_sync(0xffffffffu, lo[e], sh));
+      for (int e = 0; e < 8; ++e) {
+        const float2 a = bf2(w[e / 2]);
+        const float u = tame(e % 2 ? a.y : a.x);
+        hi[e] = fmaxf(hi[e], u);
+        lo[e] = fminf(lo[e], u);
+      }
     }
-    amax = fmaxf(amax, fmaxf(fabsf(hi[e]), fabsf(lo[e])));
+    amax = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+#pragma unroll
+      for (int sh = Y::CH; sh < 32; sh <<= 1) {
+        hi[e] = fmaxf(hi[e], __shfl_xor_sync(0xffffffffu, hi[e], sh));
+        lo[e] = fminf(lo[e], __shfl_xor_sync(0xffffffffu, lo[e], sh));
+      }
+      amax = fmaxf(amax, fmaxf(fabsf(hi[e]), fabsf(lo[e])));
+    }
+    amax = warp_max(amax);
   }
-  amax = warp_max(amax);
   const int e = unit_exponent(amax);
   const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
   if (lane == 0) *scale = __uint_as_float((uint32_t)(e + 127) << 23);
@@ -169,36 +226,55 @@ __device__ __forceinline__ int page_of(const QuantArgs& a, const int32_t* pt, in
   return -1;
 }
 
-// Work unit u of the range kernels: (sequence, page, KV head, K or V).
+// What becomes of a full page in x: codes (FMT != kNoFormat), bounds of its keys.
+template <int D, int FMT, bool KEYS>
+__device__ __forceinline__ void write_page(const QuantArgs& a, const uint4 (&x)[Lay<D>::NI], int b, int p, int h,
+                                           int lane) {
+  const Extremes ex = extremes<D, KEYS>(x);
+  if constexpr (FMT != kNoFormat) {
+    const int dst = page_of(a, a.qpt, b, p, lane, a.err);
+    if (dst >= 0) {
+      const size_t ph = (size_t)dst * a.Hkv + h;
+      write_codes<D, FMT>(x, ex.amax, lane, (KEYS ? a.kq : a.vq) + ph * (kPage * D), (KEYS ? a.ks : a.vs) + ph);
+    }
+  }
+  if constexpr (KEYS) {
+    if (a.bounds) {
+      const int ip = page_of(a, a.ipt, b, p, lane, a.err_ix);
+      if (ip >= 0) {
+        const size_t ph = (size_t)ip * a.Hkv + h;
+        write_bounds<D>(x, ex, lane, a.bounds + ph * 2 * D, a.bscale + ph);
+      }
+    }
+  }
+}
+
+// Work of warp u of sequence b = blockIdx.y in the range kernels: page, KV
+// head, K or V (per_page: units of a page).
 struct Unit {
-  int b, p, h, v;
+  int p, h, v;
 };
-__device__ __forceinline__ Unit unit_of(long u, int n_pages, int Hkv, int nkv) {
-  Unit r;
-  r.v = (int)(u % nkv);
-  u /= nkv;
-  r.h = (int)(u % Hkv);
-  u /= Hkv;
-  r.p = (int)(u % n_pages);
-  r.b = (int)(u / n_pages);
-  return r;
+__device__ __forceinline__ Unit unit_of(uint32_t u, int per_page, int nkv) {
+  const uint32_t p = u / (uint32_t)per_page, r = u - p * (uint32_t)per_page;
+  return Unit{(int)p, nkv == 2 ? (int)(r >> 1) : (int)r, nkv == 2 ? (int)(r & 1) : 0};
 }
 
 // Store: bf16 pages [page_lo, ...) of every sequence -> codes, scales, bounds;
 // the page that is not full -> tail.  FMT == kNoFormat: bounds only.
 template <int D, int FMT>
-__global__ void __launch_bounds__(256) store_kernel(const QuantArgs a, int n_pages, long units) {
+__global__ void __launch_bounds__(256) store_kernel(const QuantArgs a, int units) {
   grid_dep_enter_writer();
   using Y = Lay<D>;
-  const int lane = threadIdx.x & 31;
-  const long u = (long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (u >= units) return;
-  const Unit w = unit_of(u, n_pages, a.Hkv, FMT == kNoFormat ? 1 : 2);
-  const int len = seq_len(a.lens, a.L, w.b, a.err);
+  constexpr int nkv = FMT == kNoFormat ? 1 : 2;
+  const int lane = threadIdx.x & 31, b = blockIdx.y;
+  const uint32_t u = blockIdx.x * 8u + (threadIdx.x >> 5);
+  if (u >= (uint32_t)units) return;
+  const Unit w = unit_of(u, a.Hkv * nkv, nkv);
+  const int len = seq_len(a.lens, a.L, b, a.err);
   const int p = a.page_lo + w.p;
   const int rows = min(kPage, len - p * kPage);
   if (rows <= 0 || (FMT == kNoFormat && rows < kPage)) return;
-  const int src = page_of(a, a.pt, w.b, p, lane, a.err_kv);
+  const int src = page_of(a, a.pt, b, p, lane, a.err_kv);
   if (src < 0) return;
   const __nv_bfloat16* from = (w.v ? a.v_pool : a.k_pool) + ((size_t)src * a.Hkv + w.h) * (kPage * D);
   const int row0 = lane / Y::CH, ch = lane % Y::CH;
@@ -209,7 +285,7 @@ __global__ void __launch_bounds__(256) store_kernel(const QuantArgs a, int n_pag
     x[i] = r < rows ? __ldg(reinterpret_cast<const uint4*>(from + r * D + ch * 8)) : make_uint4(0, 0, 0, 0);
   }
   if (rows < kPage) {
-    __nv_bfloat16* tail = (w.v ? a.v_tail : a.k_tail) + ((size_t)w.b * a.Hkv + w.h) * (kPage * D);
+    __nv_bfloat16* tail = (w.v ? a.v_tail : a.k_tail) + ((size_t)b * a.Hkv + w.h) * (kPage * D);
 #pragma unroll
     for (int i = 0; i < Y::NI; ++i) {
       const int r = i * Y::RPI + row0;
@@ -217,20 +293,8 @@ __global__ void __launch_bounds__(256) store_kernel(const QuantArgs a, int n_pag
     }
     return;
   }
-  if constexpr (FMT != kNoFormat) {
-    const int dst = page_of(a, a.qpt, w.b, p, lane, a.err);
-    if (dst >= 0) {
-      const size_t ph = (size_t)dst * a.Hkv + w.h;
-      write_codes<D, FMT>(x, lane, (w.v ? a.vq : a.kq) + ph * (kPage * D), (w.v ? a.vs : a.ks) + ph);
-    }
-  }
-  if (a.bounds && !w.v) {
-    const int ip = page_of(a, a.ipt, w.b, p, lane, a.err_ix);
-    if (ip >= 0) {
-      const size_t ph = (size_t)ip * a.Hkv + w.h;
-      write_bounds<D>(x, lane, a.bounds + ph * 2 * D, a.bscale + ph);
-    }
-  }
+  if (w.v) write_page<D, FMT, false>(a, x, b, p, w.h, lane);
+  else write_page<D, FMT, true>(a, x, b, p, w.h, lane);
 }
 
 // Append: one token of every (sequence, KV head), K or V per warp.
@@ -257,18 +321,8 @@ __global__ void __launch_bounds__(128) append_quant_kernel(const QuantArgs a, in
       const int r = i * Y::RPI + row0;
       x[i] = r < kPage - 1 ? *reinterpret_cast<const uint4*>(tail + r * D + ch * 8) : t;
     }
-    const int dst = page_of(a, a.qpt, b, p, lane, a.err);
-    if (dst >= 0) {
-      const size_t ph = (size_t)dst * a.Hkv + h;
-      write_codes<D, FMT>(x, lane, (v ? a.vq : a.kq) + ph * (kPage * D), (v ? a.vs : a.ks) + ph);
-    }
-    if (a.bounds && !v) {
-      const int ip = page_of(a, a.ipt, b, p, lane, a.err_ix);
-      if (ip >= 0) {
-        const size_t ph = (size_t)ip * a.Hkv + h;
-        write_bounds<D>(x, lane, a.bounds + ph * 2 * D, a.bscale + ph);
-      }
-    }
+    if (v) write_page<D, FMT, false>(a, x, b, p, h, lane);
+    else write_page<D, FMT, true>(a, x, b, p, h, lane);
   }
   if (row0 == 0) *reinterpret_cast<uint4*>(tail + row * D + ch * 8) = t;
 }
@@ -286,23 +340,23 @@ __device__ __forceinline__ uint32_t decode2(uint32_t codes, float scale, int fmt
 
 // Load: the 8-bit pages and the tail -> bf16 pages.
 template <int D, int FMT>
-__global__ void __launch_bounds__(256) load_kernel(const QuantArgs a, int n_pages, long units) {
+__global__ void __launch_bounds__(256) load_kernel(const QuantArgs a, int units) {
   grid_dep_enter_writer();
   using Y = Lay<D>;
-  const int lane = threadIdx.x & 31;
-  const long u = (long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (u >= units) return;
-  const Unit w = unit_of(u, n_pages, a.Hkv, 2);
-  const int len = seq_len(a.lens, a.L, w.b, a.err);
+  const int lane = threadIdx.x & 31, b = blockIdx.y;
+  const uint32_t u = blockIdx.x * 8u + (threadIdx.x >> 5);
+  if (u >= (uint32_t)units) return;
+  const Unit w = unit_of(u, a.Hkv * 2, 2);
+  const int len = seq_len(a.lens, a.L, b, a.err);
   const int p = a.page_lo + w.p;
   const int rows = min(kPage, len - p * kPage);
   if (rows <= 0) return;
-  const int dst = page_of(a, a.pt, w.b, p, lane, a.err_kv);
+  const int dst = page_of(a, a.pt, b, p, lane, a.err_kv);
   if (dst < 0) return;
   __nv_bfloat16* to = (w.v ? a.v_pool : a.k_pool) + ((size_t)dst * a.Hkv + w.h) * (kPage * D);
   const int row0 = lane / Y::CH, ch = lane % Y::CH;
   if (rows < kPage) {
-    const __nv_bfloat16* tail = (w.v ? a.v_tail : a.k_tail) + ((size_t)w.b * a.Hkv + w.h) * (kPage * D);
+    const __nv_bfloat16* tail = (w.v ? a.v_tail : a.k_tail) + ((size_t)b * a.Hkv + w.h) * (kPage * D);
 #pragma unroll
     for (int i = 0; i < Y::NI; ++i) {
       const int r = i * Y::RPI + row0;
@@ -311,7 +365,7 @@ __global__ void __launch_bounds__(256) load_kernel(const QuantArgs a, int n_page
     }
     return;
   }
-  const int src = page_of(a, a.qpt, w.b, p, lane, a.err);
+  const int src = page_of(a, a.qpt, b, p, lane, a.err);
   if (src < 0) return;
   const size_t ph = (size_t)src * a.Hkv + w.h;
   const uint8_t* from = (w.v ? a.vq : a.kq) + ph * (kPage * D);
@@ -421,13 +475,13 @@ sfi_status sfi_quant_store(const sfi_shape* shape, const sfi_paged_kv* kv, const
   add_kv(a, *kv);
   add_quant(a, *qkv);
   add_index(a, index);
-  const long units = (long)shape->B * n_pages * shape->Hkv * 2;
-  const long blocks = (units + 7) / 8;
-  if (blocks > 0x7fffffffL) return SFI_ERR_SHAPE;
+  const long units = (long)n_pages * shape->Hkv * 2;   // of a sequence
+  if (units > 0x7fffff00L || shape->B > 65535) return SFI_ERR_UNSUPPORTED;
   const bool e4 = qkv->format == SFI_FMT_E4M3;
   auto k = shape->D == 128 ? (e4 ? store_kernel<128, SFI_FMT_E4M3> : store_kernel<128, SFI_FMT_INT8>)
                            : (e4 ? store_kernel<64, SFI_FMT_E4M3> : store_kernel<64, SFI_FMT_INT8>);
-  return launched(launch_k(k, dim3((unsigned)blocks), dim3(256), 0, (cudaStream_t)stream, a, n_pages, units));
+  return launched(launch_k(k, dim3((unsigned)((units + 7) / 8), shape->B), dim3(256), 0, (cudaStream_t)stream, a,
+                           (int)units));
 }
 
 sfi_status sfi_quant_append(const sfi_shape* shape, const sfi_quant_kv* qkv, const sfi_block_index* index,
@@ -463,13 +517,13 @@ sfi_status sfi_quant_load(const sfi_shape* shape, const sfi_quant_kv* qkv, const
   QuantArgs a = base_args(*shape, pos_lo, L, lens);
   add_kv(a, *kv);
   add_quant(a, *qkv);
-  const long units = (long)shape->B * n_pages * shape->Hkv * 2;
-  const long blocks = (units + 7) / 8;
-  if (blocks > 0x7fffffffL) return SFI_ERR_SHAPE;
+  const long units = (long)n_pages * shape->Hkv * 2;   // of a sequence
+  if (units > 0x7fffff00L || shape->B > 65535) return SFI_ERR_UNSUPPORTED;
   const bool e4 = qkv->format == SFI_FMT_E4M3;
   auto k = shape->D == 128 ? (e4 ? load_kernel<128, SFI_FMT_E4M3> : load_kernel<128, SFI_FMT_INT8>)
                            : (e4 ? load_kernel<64, SFI_FMT_E4M3> : load_kernel<64, SFI_FMT_INT8>);
-  return launched(launch_k(k, dim3((unsigned)blocks), dim3(256), 0, (cudaStream_t)stream, a, n_pages, units));
+  return launched(launch_k(k, dim3((unsigned)((units + 7) / 8), shape->B), dim3(256), 0, (cudaStream_t)stream, a,
+                           (int)units));
 }
 
 sfi_status sfi_block_build(const sfi_shape* shape, const sfi_paged_kv* kv, const sfi_block_index* index,
@@ -484,11 +538,11 @@ sfi_status sfi_block_build(const sfi_shape* shape, const sfi_paged_kv* kv, const
   add_kv(a, *kv);
   add_index(a, index);
   a.err = index->err;
-  const long units = (long)shape->B * n_pages * shape->Hkv;
-  const long blocks = (units + 7) / 8;
-  if (blocks > 0x7fffffffL) return SFI_ERR_SHAPE;
+  const long units = (long)n_pages * shape->Hkv;
+  if (units > 0x7fffff00L || shape->B > 65535) return SFI_ERR_UNSUPPORTED;
   auto k = shape->D == 128 ? store_kernel<128, kNoFormat> : store_kernel<64, kNoFormat>;
-  return launched(launch_k(k, dim3((unsigned)blocks), dim3(256), 0, (cudaStream_t)stream, a, n_pages, units));
+  return launched(launch_k(k, dim3((unsigned)((units + 7) / 8), shape->B), dim3(256), 0, (cudaStream_t)stream, a,
+                           (int)units));
 }
 
 sfi_status sfi_quant_poll_error(const sfi_quant_kv* qkv, int32_t* code) {
