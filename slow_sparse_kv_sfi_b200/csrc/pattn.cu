@@ -86,6 +86,15 @@ struct PageAttnArgs {
 #ifndef PA_CT2
 #define PA_CT2 3
 #endif
+#ifndef PA_AB
+#define PA_AB 0
+#endif
+#ifndef PA_A1
+#define PA_A1 1
+#endif
+#ifndef PA_A2
+#define PA_A2 1
+#endif
 #ifndef PA_W2
 #define PA_W2 4
 #endif
@@ -120,7 +129,7 @@ struct Cfg {
   // Tiles fetched into L2 ahead of their loads: one for 8-bit pages (a warp's
   // registers hold one 4 KB tile in flight, less than the latency asks for);
   // none for bf16 pages, whose tile is twice as large.
-  static constexpr int kAhead = FMT == kBf16 ? 0 : 1;
+  static constexpr int kAhead = FMT == kBf16 ? PA_AB : HM == kTwo ? PA_A2 : PA_A1;
   static constexpr int kCtas = NT == 2 ? PA_CT2 : PA_CT;                   // per SM
   static constexpr int kMerge = W * NT * 8 * (D + 8) * 4 + W * NT * 8 * 2 * 4;   // merge of the warps
   // Q fragments: registers, or (G > 8, whose accumulators take twice the

@@ -18,6 +18,10 @@ namespace {
 
 constexpr float kAmaxFloor = 7.888609052210118e-31f;   // 2^-100: smaller pages share this scale
 constexpr int kNoFormat = -1;                          // bounds only
+// Warps of a CTA of the range kernels.  Small CTAs end alone, and their place is
+// taken at once: 4 warps took 8K store + load from 94 to 90 us, ragged 32K from
+// 421 to 409, against 8.
+constexpr unsigned kRangeWarps = 4;
 
 struct QuantArgs {
   int B, Hkv, L, num_pages, max_pages;
@@ -262,12 +266,12 @@ __device__ __forceinline__ Unit unit_of(uint32_t u, int per_page, int nkv) {
 // Store: bf16 pages [page_lo, ...) of every sequence -> codes, scales, bounds;
 // the page that is not full -> tail.  FMT == kNoFormat: bounds only.
 template <int D, int FMT>
-__global__ void __launch_bounds__(256) store_kernel(const QuantArgs a, int units) {
+__global__ void __launch_bounds__(128) store_kernel(const QuantArgs a, int units) {
   grid_dep_enter_writer();
   using Y = Lay<D>;
   constexpr int nkv = FMT == kNoFormat ? 1 : 2;
   const int lane = threadIdx.x & 31, b = blockIdx.y;
-  const uint32_t u = blockIdx.x * 8u + (threadIdx.x >> 5);
+  const uint32_t u = blockIdx.x * kRangeWarps + (threadIdx.x >> 5);
   if (u >= (uint32_t)units) return;
   const Unit w = unit_of(u, a.Hkv * nkv, nkv);
   const int len = seq_len(a.lens, a.L, b, a.err);
@@ -340,11 +344,11 @@ __device__ __forceinline__ uint32_t decode2(uint32_t codes, float scale, int fmt
 
 // Load: the 8-bit pages and the tail -> bf16 pages.
 template <int D, int FMT>
-__global__ void __launch_bounds__(256) load_kernel(const QuantArgs a, int units) {
+__global__ void __launch_bounds__(128) load_kernel(const QuantArgs a, int units) {
   grid_dep_enter_writer();
   using Y = Lay<D>;
   const int lane = threadIdx.x & 31, b = blockIdx.y;
-  const uint32_t u = blockIdx.x * 8u + (threadIdx.x >> 5);
+  const uint32_t u = blockIdx.x * kRangeWarps + (threadIdx.x >> 5);
   if (u >= (uint32_t)units) return;
   const Unit w = unit_of(u, a.Hkv * 2, 2);
   const int len = seq_len(a.lens, a.L, b, a.err);
@@ -480,7 +484,7 @@ sfi_status sfi_quant_store(const sfi_shape* shape, const sfi_paged_kv* kv, const
   const bool e4 = qkv->format == SFI_FMT_E4M3;
   auto k = shape->D == 128 ? (e4 ? store_kernel<128, SFI_FMT_E4M3> : store_kernel<128, SFI_FMT_INT8>)
                            : (e4 ? store_kernel<64, SFI_FMT_E4M3> : store_kernel<64, SFI_FMT_INT8>);
-  return launched(launch_k(k, dim3((unsigned)((units + 7) / 8), shape->B), dim3(256), 0, (cudaStream_t)stream, a,
+  return launched(launch_k(k, dim3((unsigned)((units + kRangeWarps - 1) / kRangeWarps), shape->B), dim3(kRangeWarps * 32), 0, (cudaStream_t)stream, a,
                            (int)units));
 }
 
@@ -522,7 +526,7 @@ sfi_status sfi_quant_load(const sfi_shape* shape, const sfi_quant_kv* qkv, const
   const bool e4 = qkv->format == SFI_FMT_E4M3;
   auto k = shape->D == 128 ? (e4 ? load_kernel<128, SFI_FMT_E4M3> : load_kernel<128, SFI_FMT_INT8>)
                            : (e4 ? load_kernel<64, SFI_FMT_E4M3> : load_kernel<64, SFI_FMT_INT8>);
-  return launched(launch_k(k, dim3((unsigned)((units + 7) / 8), shape->B), dim3(256), 0, (cudaStream_t)stream, a,
+  return launched(launch_k(k, dim3((unsigned)((units + kRangeWarps - 1) / kRangeWarps), shape->B), dim3(kRangeWarps * 32), 0, (cudaStream_t)stream, a,
                            (int)units));
 }
 
@@ -541,7 +545,7 @@ sfi_status sfi_block_build(const sfi_shape* shape, const sfi_paged_kv* kv, const
   const long units = (long)n_pages * shape->Hkv;
   if (units > 0x7fffff00L || shape->B > 65535) return SFI_ERR_UNSUPPORTED;
   auto k = shape->D == 128 ? store_kernel<128, kNoFormat> : store_kernel<64, kNoFormat>;
-  return launched(launch_k(k, dim3((unsigned)((units + 7) / 8), shape->B), dim3(256), 0, (cudaStream_t)stream, a,
+  return launched(launch_k(k, dim3((unsigned)((units + kRangeWarps - 1) / kRangeWarps), shape->B), dim3(kRangeWarps * 32), 0, (cudaStream_t)stream, a,
                            (int)units));
 }
 
