@@ -498,7 +498,7 @@ BlockWs block_ws(const sfi_shape& s) {
   size_t off = 0;
   w.score_off = off;
   off += align_up((size_t)BH * (((size_t)s.max_pages + 3) / 4 * 4) * sizeof(float), 256);
-  const size_t items = 2 * (size_t)page_attn_ctas(BH * s.max_pages, 4);
+  const size_t items = 2 * (size_t)page_attn_ctas_bound(BH, s.max_pages);
   w.part_off = off;
   off += align_up(items * G * s.D * sizeof(float), 256);
   w.ml_off = off;

@@ -205,9 +205,9 @@ struct BlockWs {
   size_t score_off, part_off, ml_off, arrived_off, total;
 };
 BlockWs block_ws(const sfi_shape& s);
-// CTAs of an attention launch over this many tiles, at most per_sm on each
-// multiprocessor (pattn.cu); it leaves two partials per CTA.
-int page_attn_ctas(long long tiles, int per_sm);
+// The most CTAs that a page attention launch has for `rows` (sequence, KV
+// head) pairs of at most T tiles (pattn.cu); each leaves up to two partials.
+int page_attn_ctas_bound(long long rows, int T);
 sfi_status check_quant(const sfi_quant_kv* q);
 sfi_status check_index(const sfi_block_index* ix);
 

@@ -6,7 +6,9 @@
 // Work.  A tile is one page: 16 rows of K and of V.  The tiles of all rows - a
 // row being one (sequence, KV head), its tiles its pages or list entries - form
 // one sequence, and every CTA takes an equal run of it, whatever the lengths;
-// the grid is what the GPU holds at once.  A run cuts at most two rows: a row
+// the grid is what the GPU holds at once.  (Rows of one length that divide well
+// get the same number of CTAs each instead, see kSecondRow.)  A run cuts at most
+// two rows: a row
 // inside one run is finished there, the pieces of the others are merged by the
 // CTA that writes the last of them (in the order of the pieces, whoever that
 // is).  Within a row, warp w of the CTA takes tiles w, w + W, ...;
@@ -65,6 +67,7 @@ struct PageAttnArgs {
   int K;
   int total;                        // tiles of all rows, or -1: by lens
   int quota;                        // tiles of a CTA's run (total >= 0)
+  int pieces;                       // > 0: CTAs of each row, whose runs begin with the row; 0: even runs
   float scale_log2;                 // log2(e) / sqrt(D)
   float* out;
   float* lse;
@@ -107,6 +110,7 @@ struct PageAttnArgs {
 #ifndef PA_WAVES
 #define PA_WAVES 1
 #endif
+constexpr int kMaxCtas = 3;   // CTAs per SM
 enum HeadMap : int { kHalf = 0, kOne = 1, kTwo = 2 };
 
 template <int D, int FMT, int HM>
@@ -130,7 +134,8 @@ struct Cfg {
   // registers hold one 4 KB tile in flight, less than the latency asks for);
   // none for bf16 pages, whose tile is twice as large.
   static constexpr int kAhead = FMT == kBf16 ? PA_AB : HM == kTwo ? PA_A2 : PA_A1;
-  static constexpr int kCtas = NT == 2 ? PA_CT2 : PA_CT;                   // per SM
+  static constexpr int kCtas = NT == 2 ? PA_CT2 : PA_CT;   // per SM
+  static_assert(kCtas <= kMaxCtas, "the workspace has two partials for each CTA of a wave");
   static constexpr int kMerge = W * NT * 8 * (D + 8) * 4 + W * NT * 8 * 2 * 4;   // merge of the warps
   // Q fragments: registers, or (G > 8, whose accumulators take twice the
   // registers) 16 bytes of shared memory per thread, column tile and two steps.
@@ -445,10 +450,10 @@ constexpr int kMaxGroups = 8;
 
 // Tiles [t0, t1) of the T tiles of row (b, h), by the whole CTA: the row's
 // output, or (not the whole row) its piece, and the output too if that is the
-// last.  row0: the row's first tile among all.
+// last.  c0, c1: the first and last CTA with a piece of the row.
 template <int D, int FMT, int HM, bool LIST>
 __device__ __forceinline__ void attend_row(const PageAttnArgs& a, uint8_t* smem, int b, int h, int len, int T, int t0,
-                                           int t1, int row0, int quota_) {
+                                           int t1, int c0, int c1) {
   using C = Cfg<D, FMT, HM>;
   constexpr int NT = C::NT, W = C::W, KJ = C::KJ, VC = C::VC;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -793,7 +798,6 @@ __device__ __forceinline__ void attend_row(const PageAttnArgs& a, uint8_t* smem,
   if (whole) return;
 
   // The CTA that writes a row's last piece merges them all.
-  const int c0 = (int)((unsigned)row0 / (unsigned)quota_), c1 = (int)((unsigned)(row0 + T - 1) / (unsigned)quota_);
   __syncthreads();   // the piece is written
   int* last = reinterpret_cast<int*>(sml);   // the warps' (m, l) are used up
   if (threadIdx.x == 0) {
@@ -854,26 +858,44 @@ __global__ void __launch_bounds__(Cfg<D, FMT, HM>::W * 32, Cfg<D, FMT, HM>::kCta
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   grid_dep_enter();   // the next launch may come up while this one runs; it waits before it touches memory
   // this CTA's run: `left` tiles from tile t0 of row (b, h) on, whose first tile is row0
-  const int total = count_tiles(a, lane, warp == 0 ? a.err : nullptr);
-  const int run = a.total >= 0 ? a.quota : quota(total, gridDim.x);
-  int b, h, t0, row0;
-  const int pos = (int)min((long long)run * blockIdx.x, (long long)total);
-  int left = min(run, total - pos);
-  if (left > 0) {
-    int first;
-    find_sequence<LIST>(a, pos, lane, b, first);
-    const int T = row_tiles<LIST>(a, b, nullptr);
-    h = (int)((unsigned)(pos - first) / (unsigned)T);
-    row0 = first + h * T;
-    t0 = pos - row0;
+  int b, h, t0, left, row0 = 0, run;
+  if (a.pieces > 0) {
+    const int T = row_tiles<LIST>(a, 0, nullptr);
+    const unsigned row = blockIdx.x / (unsigned)a.pieces;
+    run = a.quota;
+    b = (int)(row / (unsigned)a.Hkv);
+    h = (int)row - b * a.Hkv;
+    t0 = (int)(blockIdx.x - row * a.pieces) * run;
+    left = min(run, T - t0);
+  } else {
+    const int total = count_tiles(a, lane, warp == 0 ? a.err : nullptr);
+    run = a.total >= 0 ? a.quota : quota(total, gridDim.x);
+    const int pos = (int)min((long long)run * blockIdx.x, (long long)total);
+    left = min(run, total - pos);
+    if (left > 0) {
+      int first;
+      find_sequence<LIST>(a, pos, lane, b, first);
+      const int T = row_tiles<LIST>(a, b, nullptr);
+      h = (int)((unsigned)(pos - first) / (unsigned)T);
+      row0 = first + h * T;
+      t0 = pos - row0;
+    }
   }
   for (; left > 0; ++b, h = 0) {   // sequences
-    const int len = seq_len(a.lens, a.L, b, nullptr);
+    const int len = seq_len(a.lens, a.L, b, LIST && a.lens && warp == 0 ? a.err : nullptr);
     const int T = LIST ? a.K : (len + kPage - 1) / kPage;
     if (T == 0) continue;
     for (; h < a.Hkv && left > 0; ++h) {   // rows
       const int t1 = min(T, t0 + left);
-      attend_row<D, FMT, HM, LIST>(a, smem, b, h, len, T, t0, t1, row0, run);
+      int c0, c1;
+      if (a.pieces > 0) {
+        c0 = (b * a.Hkv + h) * a.pieces;
+        c1 = c0 + a.pieces - 1;
+      } else {
+        c0 = (int)((unsigned)row0 / (unsigned)run);
+        c1 = (int)((unsigned)(row0 + T - 1) / (unsigned)run);
+      }
+      attend_row<D, FMT, HM, LIST>(a, smem, b, h, len, T, t0, t1, c0, c1);
       left -= t1 - t0;
       row0 += T;
       t0 = 0;
@@ -901,6 +923,17 @@ sfi_status cuda_status(cudaError_t e) {
   return SFI_ERR_CUDA;
 }
 
+// Rows of one length: a CTA whose run goes on into a second row spends about as
+// long on the change (its pipeline drains, a piece is written, the next row's
+// queries and pages are looked up: 3 to 4 us) as on kSecondRow tiles.  So the
+// rows get the same number of CTAs each where that makes no run longer by more.
+// Measured, us, even runs against this: 1K int8 10.4 -> 8.0, 8K e4m3 25.4 ->
+// 23.5, blocks 128K 62.3 -> 60.1.
+#ifndef PA_SR
+#define PA_SR 16
+#endif
+constexpr int kSecondRow = PA_SR;
+
 template <int D, int FMT, int HM, bool LIST>
 sfi_status launch(PageAttnArgs& a, cudaStream_t st) {
   using C = Cfg<D, FMT, HM>;
@@ -913,9 +946,22 @@ sfi_status launch(PageAttnArgs& a, cudaStream_t st) {
   const int T = LIST ? a.K : (a.L + kPage - 1) / kPage;
   const long long total = (long long)a.B * a.Hkv * T;
   if (total > 0x7fffffffLL) return SFI_ERR_SHAPE;
-  const int ctas = page_attn_ctas(total, C::kCtas);
+  // one wave, fewer CTAs where the tiles would not give each kMinQuota
+  const int wave = num_sms() * C::kCtas;
+  int ctas = (int)std::min((long long)wave, (total + kMinQuota - 1) / kMinQuota);
   a.total = !LIST && a.lens ? -1 : (int)total;
   a.quota = quota((int)total, ctas);
+  a.pieces = 0;
+  const int rows = a.B * a.Hkv;
+  if (a.total >= 0 && rows <= wave) {
+    const int p = wave / rows;
+    const int run = std::max((T + p - 1) / p, kMinQuota);
+    if (run <= a.quota + kSecondRow) {
+      a.quota = run;
+      a.pieces = (T + run - 1) / run;
+      ctas = rows * a.pieces;
+    }
+  }
   return cuda_status(launch_k(k, dim3(ctas), dim3(C::W * 32), C::kSmem, st, a));
 }
 
@@ -996,10 +1042,10 @@ sfi_status run(const sfi_shape* shape, const sfi_paged_kv* kv, const sfi_quant_k
 
 }  // namespace
 
-// One wave of `per_sm` CTAs a multiprocessor, fewer where the tiles would not
-// give each kMinQuota.
-int page_attn_ctas(long long tiles, int per_sm) {
-  return (int)std::max(1LL, std::min((long long)num_sms() * per_sm * PA_WAVES, (tiles + kMinQuota - 1) / kMinQuota));
+// Even runs take at most ceil(total / kMinQuota) CTAs and equal shares of the
+// rows at most ceil(T / kMinQuota) each, both at most one wave.
+int page_attn_ctas_bound(long long rows, int T) {
+  return (int)std::min((long long)num_sms() * kMaxCtas, rows * ((T + kMinQuota - 1) / kMinQuota));
 }
 
 }  // namespace sfi

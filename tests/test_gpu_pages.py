@@ -662,3 +662,31 @@ def test_select_uneven_scores(what, nb, K):
     torch.cuda.synchronize()
     assert int(err.item()) == (5 | (14 << 8) if what == "bad page" else 0)
     assert np.array_equal(sel[0, 0].cpu().numpy(), P.select(u, n, 4, 20, K))
+
+
+@pytest.mark.parametrize("B,Hq,Hkv,L", [(25, 16, 4, 272), (100, 3, 3, 33), (297, 1, 1, 300), (1, 16, 1, 9000), (7, 64, 4, 700),
+                                        (2, 8, 8, 17)])
+def test_calls_stay_inside_their_workspace(B, Hq, Hkv, L):
+    """Rows of every count, cut into pieces or not, of one length and ragged: nothing behind the
+    reported size is written, and the results stand."""
+    c = Case(B, Hq, Hkv, 64, [L] * B, "int8", seed=19).up()
+    need = c.ws.numel()
+    big = torch.zeros(need + (1 << 20), dtype=torch.uint8, device=DEV)
+    big[need:] = 0x3C
+    c.ws = big[:need]
+    S.sfi_quant_store(c.shape, c.kv, c.q8, 0, L, index=c.ix)
+    nb = -(-L // PAGE)
+    sel = torch.arange(nb, dtype=torch.int32, device=DEV).expand(B, Hkv, nb).contiguous()
+    outs = []
+    for lens in (None, c.lend):
+        S.sfi_quant_attn(c.shape, c.q8, L, c.qd, c.out, c.ws, lens=lens, lse=c.lse)
+        outs.append(c.out.clone())
+        S.sfi_quant_block_attn(c.shape, c.q8, L, c.qd, sel, nb, c.out, c.ws, lens=lens, lse=c.lse)
+        outs.append(c.out.clone())
+        few = torch.empty(B, Hkv, min(nb, 3), dtype=torch.int32, device=DEV)
+        S.sfi_block_select(c.shape, c.ix, L, c.qd, 0, 1, min(nb, 3), few, c.ws, lens=lens)
+    assert c.error() == 0
+    assert (big[need:] == 0x3C).all()
+    check_all(c, lambda b, h, n: c.quant_rows("k", b, h, n), lambda b, h, n: c.quant_rows("v", b, h, n))
+    for o in outs[:-1]:   # all of them attend to everything; the cuts differ
+        assert float((o - outs[-1]).abs().max()) <= 1e-5 * float(c.v.float().abs().max())
