@@ -5,29 +5,32 @@
 //
 // Work.  A tile is one page: 16 rows of K and of V.  The tiles of all rows - a
 // row being one (sequence, KV head), its tiles its pages or list entries - form
-// one sequence, and every CTA takes an equal run of it, whatever the lengths;
-// the grid is what the GPU holds at once.  (Rows of one length that divide well
-// get the same number of CTAs each instead, see kSecondRow.)  A run cuts at most
-// two rows: a row
+// one sequence, and every CTA takes an equal run of it, whatever the lengths
+// (a row counts for some tiles more than it has, see Cfg::kRowCost); the grid is
+// what the GPU holds at once.  Rows of one length that divide well get the same
+// number of CTAs each instead, see launch().  A run cuts at most two rows: a row
 // inside one run is finished there, the pieces of the others are merged by the
-// CTA that writes the last of them (in the order of the pieces, whoever that
-// is).  Within a row, warp w of the CTA takes tiles w, w + W, ...;
-// each warp runs its own online softmax and the CTA merges its warps in shared
-// memory.
+// CTA that writes the last of them, in the order of the pieces, whoever that is.
+// Within a row, warp w of the CTA takes tiles w, w + W, ...; each warp runs its
+// own online softmax and the CTA merges its warps in shared memory.
 //
-// Bound by reading the cache, so the layout serves the loads.  Each thread loads
-// exactly the bytes its own matrix fragments need, 16 at a time, straight into
-// registers: the next tile's K while the softmax and V^T P^T of this one run,
-// its V while the next S^T does.  No shared memory, no barrier and no wait that
-// another warp has to end.  That works because the order of a contraction is
-// free:
+// Bound by reading the cache (at G <= 8; at G = 16 about as much by issuing 350
+// to 400 instructions a tile), so the layout serves the loads.  Each thread loads
+// exactly the bytes its own matrix fragments need, 32 or 16 at a time, straight
+// into registers: the next tile's K while the softmax and V^T P^T of this one
+// run, its V while the next S^T does.  No shared memory, no barrier and no wait
+// that another warp has to end.  That works because the order of a contraction
+// is free:
 //   S^T[16 tok x 8 heads] = K[16 x D] . Q^T[D x 8]: thread (g, t) of the
 //     fragment layout (g = lane / 4, t = lane % 4) holds rows g, g + 8 and any
-//     D / 4 of the columns, as long as Q is laid out alike: the 16-byte chunks
-//     t, t + 4, ... of the row;
+//     D / 4 of the columns, as long as Q is laid out alike: a run of them, so
+//     that a warp's load covers whole rows;
 //   O^T[D x 8 heads] += V^T[D x 16] . P^T[16 x 8]: it holds tokens 2t, 2t + 1,
 //     2t + 8, 2t + 9 and a run of D / 8 columns of each; two tokens' bytes are
 //     interleaved into the 16-bit pairs that the fragment wants.
+// (A ring of stages in shared memory, filled by asynchronous copies, took 127 us
+// for the 128K e4m3 case where this took 117: its copies and reads back kept the
+// shared-memory pipe busy and the warps waiting for it.)
 // 8-bit codes become fp16 in registers, exactly (int8 and e4m3 both fit), and Q
 // fp16 times a power of two per head; the key scale multiplies the logits, the
 // value scale the tile's product.  P is split into hi + lo, which keeps 22 bits
@@ -65,8 +68,9 @@ struct PageAttnArgs {
   const int32_t* sel;               // LIST
   int64_t sel_ld;
   int K;
-  int total;                        // tiles of all rows, or -1: by lens
-  int quota;                        // tiles of a CTA's run (total >= 0)
+  int total;                        // units of all rows (row_units), or -1: by lens
+  int quota;                        // units of a CTA's run (total >= 0)
+  int row_cost;                     // units of a row besides its tiles
   int pieces;                       // > 0: CTAs of each row, whose runs begin with the row; 0: even runs
   float scale_log2;                 // log2(e) / sqrt(D)
   float* out;
@@ -80,36 +84,8 @@ struct PageAttnArgs {
 // HM, how the group's heads fill the 8 columns of a product: kHalf (G <= 4) has
 // heads 0 .. 3 twice, the second time with the low part of P, so one product
 // serves both parts; kOne (G <= 8) and kTwo (G <= 16) take hi and lo in turn.
-#ifndef PA_W
-#define PA_W 8
-#endif
-#ifndef PA_WB
-#define PA_WB 6
-#endif
-#ifndef PA_CT2
-#define PA_CT2 3
-#endif
-#ifndef PA_AB
-#define PA_AB 0
-#endif
-#ifndef PA_A1
-#define PA_A1 1
-#endif
-#ifndef PA_A2
-#define PA_A2 1
-#endif
-#ifndef PA_W2
-#define PA_W2 4
-#endif
-#ifndef PA_CT
-#define PA_CT 2
-#endif
-#ifndef PA_MINQ
-#define PA_MINQ 16
-#endif
-#ifndef PA_WAVES
-#define PA_WAVES 1
-#endif
+// (G = 4 through kOne against kHalf, us: 128K int8 96.3, 93.2; D = 64 128K e4m3
+// 117, 115; 128K e4m3 89.8, 90.1.)
 constexpr int kMaxCtas = 3;   // CTAs per SM
 enum HeadMap : int { kHalf = 0, kOne = 1, kTwo = 2 };
 
@@ -129,13 +105,27 @@ struct Cfg {
     return kEl == 2 ? (k / 4) * 64 + t * 16 + (k % 4) * 4 : KJ == 2 ? t * 32 + k * 4 : t * 16 + k * 4;
   }
   static __device__ __forceinline__ int v_col(int g, int k) { return g * (D / 8) + 2 * k; }
-  static constexpr int W = NT == 2 ? PA_W2 : FMT == kBf16 ? PA_WB : PA_W;   // warps
-  // Tiles fetched into L2 ahead of their loads: one for 8-bit pages (a warp's
-  // registers hold one 4 KB tile in flight, less than the latency asks for);
-  // none for bf16 pages, whose tile is twice as large.
-  static constexpr int kAhead = FMT == kBf16 ? PA_AB : HM == kTwo ? PA_A2 : PA_A1;
-  static constexpr int kCtas = NT == 2 ? PA_CT2 : PA_CT;   // per SM
+  // Warps and CTAs per SM: as many warps as the registers allow.  us at 128K
+  // e4m3: 8 x 2 93, 7 x 2 103; blocks 128K (bf16, whose tile takes twice the
+  // registers): 6 x 2 62, 5 x 2 63, 7 x 2 65; 64K x 16 heads: 4 x 3 264, 5 x 2
+  // 261, 6 x 2 264, 4 x 2 294.
+  static constexpr int W = NT == 2 ? 4 : FMT == kBf16 ? 6 : 8;
+  static constexpr int kCtas = NT == 2 ? 3 : 2;
   static_assert(kCtas <= kMaxCtas, "the workspace has two partials for each CTA of a wave");
+  // Tiles fetched into L2 ahead of their loads: one for 8-bit pages (a warp's
+  // registers hold one 4 KB tile in flight, less than the latency asks for),
+  // none for bf16 pages, whose tile is twice as large.  us with 0, 1, 2 ahead:
+  // 128K e4m3 97, 93, 96; blocks 128K 62, 64.
+  static constexpr int kAhead = FMT == kBf16 ? 0 : 1;
+  // What a row costs a CTA besides its tiles, in tiles: queries and pages looked
+  // up, the pipeline filled and drained, the warps merged, about 3 us (twice as
+  // long a tile for G > 8).  Runs of equal tile counts alone gave the CTAs with
+  // many short rows most to do: 64 sequences of 25 to 1600 tokens and 8 heads
+  // took 57 us, in the order of their lengths 106; with 24 units a row, 34 and
+  // 34 (12: 37, 38; 16: 36, 35).
+  static constexpr int kRowCost = NT == 2 ? 12 : 24;
+  // and what a second row costs a run that goes on into it
+  static constexpr int kSecondRow = NT == 2 ? 8 : 16;
   static constexpr int kMerge = W * NT * 8 * (D + 8) * 4 + W * NT * 8 * 2 * 4;   // merge of the warps
   // Q fragments: registers, or (G > 8, whose accumulators take twice the
   // registers) 16 bytes of shared memory per thread, column tile and two steps.
@@ -150,23 +140,27 @@ __device__ __forceinline__ int row_tiles(const PageAttnArgs& a, int b, int* err)
   return LIST ? a.K : (seq_len(a.lens, a.L, b, err) + kPage - 1) / kPage;
 }
 
-// The run of each CTA is `quota` tiles of the whole sequence of `total` tiles;
-// a smaller one than kMinQuota would not fill the warps of a CTA.
-constexpr int kMinQuota = PA_MINQ;
-__host__ __device__ __forceinline__ int quota(int total, int ctas) {
+// Units of a row: its tiles, after row_cost units for what a row costs a CTA
+// besides them (see Cfg::kRowCost).
+__host__ __device__ __forceinline__ int row_units(int tiles, int row_cost) { return tiles > 0 ? tiles + row_cost : 0; }
+
+// The run of each CTA, in units, of `total` units.  A run of fewer than
+// kMinQuota tiles would not fill the warps of a CTA.
+constexpr int kMinQuota = 16;   // us at 1K with 8, 16, 32: attention 7.0, 7.5, 12; block decode 13, 10.9, 10.8
+__host__ __device__ __forceinline__ int quota(int total, int ctas, int row_cost) {
   const int q = (int)(((unsigned)total + (unsigned)ctas - 1u) / (unsigned)ctas);
-  return q > kMinQuota ? q : kMinQuota;
+  return q > kMinQuota + row_cost ? q : kMinQuota + row_cost;
 }
 
-// Tiles of all rows (one warp; all lanes get it).
-__device__ __forceinline__ int count_tiles(const PageAttnArgs& a, int lane, int* err) {
+// Units of all rows (one warp; all lanes get it).
+__device__ __forceinline__ int count_units(const PageAttnArgs& a, int lane, int* err) {
   if (a.total >= 0) return a.total;   // rows of one length
   int t = 0;
-  for (int i = lane; i < a.B; i += 32) t += row_tiles<false>(a, i, err);
+  for (int i = lane; i < a.B; i += 32) t += row_units(row_tiles<false>(a, i, err), a.row_cost);
   return (int)__reduce_add_sync(0xffffffffu, (unsigned)t) * a.Hkv;
 }
 
-// The sequence whose rows hold tile `pos` (< total) and the first tile of its
+// The sequence whose rows hold unit `pos` (< total) and the first unit of its
 // rows (one warp; all lanes get both).
 template <bool LIST>
 __device__ __forceinline__ void find_sequence(const PageAttnArgs& a, int pos, int lane, int& b, int& first) {
@@ -179,7 +173,7 @@ __device__ __forceinline__ void find_sequence(const PageAttnArgs& a, int pos, in
   int base = 0;
   for (int i0 = 0; i0 < a.B; i0 += 32) {
     const int i = i0 + lane;
-    const int v = i < a.B ? row_tiles<LIST>(a, i, nullptr) * a.Hkv : 0;
+    const int v = i < a.B ? row_units(row_tiles<LIST>(a, i, nullptr), a.row_cost) * a.Hkv : 0;
     int x = v;
 #pragma unroll
     for (int sh = 1; sh < 32; sh <<= 1) {
@@ -540,11 +534,15 @@ __device__ __forceinline__ void attend_row(const PageAttnArgs& a, uint8_t* smem,
     }
     x.page = __shfl_sync(0xffffffffu, mine.page, i & 31);
     x.rows = __shfl_sync(0xffffffffu, mine.rows, i & 31);
+    return x;
+  };
+  // the scales of tile i, before tile_at(i + 1): their loads are not waited for
+  // ahead of the first loads of K and V
+  auto scales_at = [&](Tile& x, int i) {
     if (FMT != kBf16) {
       x.ks = __shfl_sync(0xffffffffu, mine.ks, i & 31);
       x.vs = __shfl_sync(0xffffffffu, mine.vs, i & 31);
     }
-    return x;
   };
   uint4 kx[2 * KJ], vx[4 * VC];
   const uint8_t* k0 = a.k + (size_t)h * C::kTile + g * C::kRow + t * C::KL;
@@ -647,6 +645,7 @@ __device__ __forceinline__ void attend_row(const PageAttnArgs& a, uint8_t* smem,
     }
   }
   for (int i = 0; i < n; ++i) {
+    scales_at(cur, i);
     const Tile nxt = tile_at(i + 1);
     auto next_k = [&]() {
       if (nxt.page >= 0) load_k(nxt);
@@ -857,49 +856,52 @@ __global__ void __launch_bounds__(Cfg<D, FMT, HM>::W * 32, Cfg<D, FMT, HM>::kCta
   extern __shared__ __align__(16) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   grid_dep_enter();   // the next launch may come up while this one runs; it waits before it touches memory
-  // this CTA's run: `left` tiles from tile t0 of row (b, h) on, whose first tile is row0
-  int b, h, t0, left, row0 = 0, run;
+  // this CTA's run: `left` units from unit v0 of row (b, h) on, whose first unit is row0
+  int b, h, v0, left, row0 = 0, run;
   if (a.pieces > 0) {
     const int T = row_tiles<LIST>(a, 0, nullptr);
     const unsigned row = blockIdx.x / (unsigned)a.pieces;
     run = a.quota;
     b = (int)(row / (unsigned)a.Hkv);
     h = (int)row - b * a.Hkv;
-    t0 = (int)(blockIdx.x - row * a.pieces) * run;
-    left = min(run, T - t0);
+    v0 = a.row_cost + (int)(blockIdx.x - row * a.pieces) * run;
+    left = min(run, T + a.row_cost - v0);
   } else {
-    const int total = count_tiles(a, lane, warp == 0 ? a.err : nullptr);
-    run = a.total >= 0 ? a.quota : quota(total, gridDim.x);
+    const int total = count_units(a, lane, warp == 0 ? a.err : nullptr);
+    run = a.total >= 0 ? a.quota : quota(total, gridDim.x, a.row_cost);
     const int pos = (int)min((long long)run * blockIdx.x, (long long)total);
     left = min(run, total - pos);
     if (left > 0) {
       int first;
       find_sequence<LIST>(a, pos, lane, b, first);
-      const int T = row_tiles<LIST>(a, b, nullptr);
-      h = (int)((unsigned)(pos - first) / (unsigned)T);
-      row0 = first + h * T;
-      t0 = pos - row0;
+      const int V = row_units(row_tiles<LIST>(a, b, nullptr), a.row_cost);
+      h = (int)((unsigned)(pos - first) / (unsigned)V);
+      row0 = first + h * V;
+      v0 = pos - row0;
     }
   }
   for (; left > 0; ++b, h = 0) {   // sequences
     const int len = seq_len(a.lens, a.L, b, LIST && a.lens && warp == 0 ? a.err : nullptr);
     const int T = LIST ? a.K : (len + kPage - 1) / kPage;
     if (T == 0) continue;
+    const int V = row_units(T, a.row_cost);
     for (; h < a.Hkv && left > 0; ++h) {   // rows
-      const int t1 = min(T, t0 + left);
-      int c0, c1;
-      if (a.pieces > 0) {
-        c0 = (b * a.Hkv + h) * a.pieces;
-        c1 = c0 + a.pieces - 1;
-      } else {
-        c0 = (int)((unsigned)row0 / (unsigned)run);
-        c1 = (int)((unsigned)(row0 + T - 1) / (unsigned)run);
+      const int v1 = min(V, v0 + left);
+      if (v1 > a.row_cost) {   // else none of its tiles
+        int c0, c1;
+        if (a.pieces > 0) {
+          c0 = (b * a.Hkv + h) * a.pieces;
+          c1 = c0 + a.pieces - 1;
+        } else {
+          c0 = (int)((unsigned)(row0 + a.row_cost) / (unsigned)run);
+          c1 = (int)((unsigned)(row0 + V - 1) / (unsigned)run);
+        }
+        attend_row<D, FMT, HM, LIST>(a, smem, b, h, len, T, max(0, v0 - a.row_cost), v1 - a.row_cost, c0, c1);
+        __syncthreads();   // the row's shared memory is free
       }
-      attend_row<D, FMT, HM, LIST>(a, smem, b, h, len, T, t0, t1, c0, c1);
-      left -= t1 - t0;
-      row0 += T;
-      t0 = 0;
-      __syncthreads();   // the row's shared memory is free
+      left -= v1 - v0;
+      row0 += V;
+      v0 = 0;
     }
   }
   if (a.total < 0) {   // the outputs of empty sequences
@@ -923,17 +925,9 @@ sfi_status cuda_status(cudaError_t e) {
   return SFI_ERR_CUDA;
 }
 
-// Rows of one length: a CTA whose run goes on into a second row spends about as
-// long on the change (its pipeline drains, a piece is written, the next row's
-// queries and pages are looked up: 3 to 4 us) as on kSecondRow tiles.  So the
-// rows get the same number of CTAs each where that makes no run longer by more.
-// Measured, us, even runs against this: 1K int8 10.4 -> 8.0, 8K e4m3 25.4 ->
-// 23.5, blocks 128K 62.3 -> 60.1.
-#ifndef PA_SR
-#define PA_SR 16
-#endif
-constexpr int kSecondRow = PA_SR;
-
+// Rows of one length get the same number of CTAs each where that makes no run
+// longer by more than kSecondRow.  Measured, us, even runs against
+// this: 1K int8 10.6 -> 7.5, 8K e4m3 25.3 -> 21.8, 128K e4m3 94.5 -> 89.8.
 template <int D, int FMT, int HM, bool LIST>
 sfi_status launch(PageAttnArgs& a, cudaStream_t st) {
   using C = Cfg<D, FMT, HM>;
@@ -944,19 +938,20 @@ sfi_status launch(PageAttnArgs& a, cudaStream_t st) {
     if (!once.mark(e)) return cuda_status(e);
   }
   const int T = LIST ? a.K : (a.L + kPage - 1) / kPage;
-  const long long total = (long long)a.B * a.Hkv * T;
+  const long long total = (long long)a.B * a.Hkv * row_units(T, C::kRowCost);
   if (total > 0x7fffffffLL) return SFI_ERR_SHAPE;
   // one wave, fewer CTAs where the tiles would not give each kMinQuota
   const int wave = num_sms() * C::kCtas;
-  int ctas = (int)std::min((long long)wave, (total + kMinQuota - 1) / kMinQuota);
+  int ctas = (int)std::min((long long)wave, (total + kMinQuota + C::kRowCost - 1) / (kMinQuota + C::kRowCost));
   a.total = !LIST && a.lens ? -1 : (int)total;
-  a.quota = quota((int)total, ctas);
+  a.quota = quota((int)total, ctas, C::kRowCost);
+  a.row_cost = C::kRowCost;
   a.pieces = 0;
   const int rows = a.B * a.Hkv;
   if (a.total >= 0 && rows <= wave) {
     const int p = wave / rows;
     const int run = std::max((T + p - 1) / p, kMinQuota);
-    if (run <= a.quota + kSecondRow) {
+    if (run <= a.quota + C::kSecondRow) {
       a.quota = run;
       a.pieces = (T + run - 1) / run;
       ctas = rows * a.pieces;
