@@ -479,7 +479,7 @@ cudaError_t launch_select(const SelectArgs& a, int BH, int cs, cudaStream_t st) 
   attr[1].val.clusterDim.x = cs;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
+  cfg.numAttrs = cs > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, k, a);
 }
 

@@ -187,10 +187,11 @@ def make_packed(k, v, pos, headmask, n_rows) -> Packed:
                   n_rows.data_ptr(), k.shape[2])
 
 
-def _arg(t, name, dtypes, shape=None):
-    """Checks a tensor argument of the 8-bit and block calls and returns its address."""
+def _arg(t, name, dtypes, shape=None, dev=None):
+    """Checks a tensor argument of the 8-bit and block calls (dev: the current device, where known) and
+    returns its address."""
     if (t.dtype in dtypes and (shape is None or t.shape == shape) and t.is_contiguous()
-            and t.is_cuda and t.get_device() == torch.cuda.current_device()):
+            and t.is_cuda and t.get_device() == (torch.cuda.current_device() if dev is None else dev)):
         return t.data_ptr()
     if t.dtype not in dtypes:
         raise ValueError(f"{name}: dtype {t.dtype}, expected {' or '.join(str(d) for d in dtypes)}")
@@ -204,12 +205,12 @@ def _arg(t, name, dtypes, shape=None):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _on(stream):
+def _on(stream, dev):
     """The stream handle of a call: the given stream or the current one, read
     without building a Stream object where torch allows it (3 us of a call)."""
     if stream is None:
         if _raw_stream is not None:
-            return _raw_stream(torch.cuda.current_device())
+            return _raw_stream(dev)
         stream = torch.cuda.current_stream()
     return stream.cuda_stream
 
@@ -255,24 +256,25 @@ def _dims(shape, *parts):
             raise ValueError(f"{type(x).__name__} has (B, Hkv, D, max_pages, num_pages) {x.dims}, the shape {want}")
 
 
-def _lens(shape, lens):
-    return None if lens is None else _arg(lens, "lens", _I32, (shape.B,))
+def _lens(B, lens, dev):
+    return None if lens is None else _arg(lens, "lens", _I32, (B,), dev)
 
 
-def _attn_args(shape, q, out, lse):
-    qs = (shape.B, shape.Hq, shape.D)
-    return (_arg(q, "q", _BF16, qs), _arg(out, "out", _F32, qs),
-            None if lse is None else _arg(lse, "lse", _F32, qs[:2]))
+def _attn_args(shape, q, out, lse, dev):
+    b, hq = shape.B, shape.Hq
+    qs = (b, hq, shape.D)
+    return (_arg(q, "q", _BF16, qs, dev), _arg(out, "out", _F32, qs, dev),
+            None if lse is None else _arg(lse, "lse", _F32, (b, hq), dev))
 
 
-def _sel(shape, sel):
+def _sel(shape, sel, dev):
     if sel.dim() != 3 or sel.shape[0] != shape.B or sel.shape[1] != shape.Hkv:
         raise ValueError(f"sel: shape {tuple(sel.shape)}, expected ({shape.B}, {shape.Hkv}, at least K)")
-    return _arg(sel, "sel", _I32)
+    return _arg(sel, "sel", _I32, None, dev)
 
 
-def _ws(ws):
-    return _arg(ws, "ws", (ws.dtype,)), ws.numel() * ws.element_size()
+def _ws(ws, dev):
+    return _arg(ws, "ws", (ws.dtype,), None, dev), ws.numel() * ws.element_size()
 
 
 # ---------------------------------------------------------------- entry points
@@ -407,30 +409,34 @@ def sfi_selftest_wait(kv, limit_ns: int, stream=None):
 
 # ---------------------------------------------------------------- 8-bit cache, block-sparse attention
 def sfi_quant_store(shape, kv, qkv, pos_lo, L, lens=None, index=None, stream=None):
+    dev = torch.cuda.current_device()
     _dims(shape, qkv, index)
     _check(lib().sfi_quant_store(C.byref(shape), C.byref(kv), C.byref(qkv), _ref(index), pos_lo, L,
-                                 _lens(shape, lens), _on(stream)), "sfi_quant_store")
+                                 _lens(shape.B, lens, dev), _on(stream, dev)), "sfi_quant_store")
 
 
 def sfi_quant_append(shape, qkv, L, k_new, v_new, lens=None, index=None, stream=None):
+    dev = torch.cuda.current_device()
     _dims(shape, qkv, index)
     tok = (shape.B, shape.Hkv, shape.D)
-    _check(lib().sfi_quant_append(C.byref(shape), C.byref(qkv), _ref(index), L, _lens(shape, lens),
-                                  _arg(k_new, "k_new", _BF16, tok), _arg(v_new, "v_new", _BF16, tok),
-                                  _on(stream)), "sfi_quant_append")
+    _check(lib().sfi_quant_append(C.byref(shape), C.byref(qkv), _ref(index), L, _lens(shape.B, lens, dev),
+                                  _arg(k_new, "k_new", _BF16, tok, dev), _arg(v_new, "v_new", _BF16, tok, dev),
+                                  _on(stream, dev)), "sfi_quant_append")
 
 
 def sfi_quant_load(shape, qkv, kv, pos_lo, L, lens=None, stream=None):
+    dev = torch.cuda.current_device()
     _dims(shape, qkv)
-    _check(lib().sfi_quant_load(C.byref(shape), C.byref(qkv), C.byref(kv), pos_lo, L, _lens(shape, lens),
-                                _on(stream)), "sfi_quant_load")
+    _check(lib().sfi_quant_load(C.byref(shape), C.byref(qkv), C.byref(kv), pos_lo, L, _lens(shape.B, lens, dev),
+                                _on(stream, dev)), "sfi_quant_load")
 
 
 def sfi_quant_attn(shape, qkv, L, q, out, ws, lens=None, lse=None, stream=None):
+    dev = torch.cuda.current_device()
     _dims(shape, qkv)
-    q, out, lse = _attn_args(shape, q, out, lse)
-    _check(lib().sfi_quant_attn(C.byref(shape), C.byref(qkv), L, _lens(shape, lens), q, out, lse, *_ws(ws),
-                                _on(stream)), "sfi_quant_attn")
+    q, out, lse = _attn_args(shape, q, out, lse, dev)
+    _check(lib().sfi_quant_attn(C.byref(shape), C.byref(qkv), L, _lens(shape.B, lens, dev), q, out, lse,
+                                *_ws(ws, dev), _on(stream, dev)), "sfi_quant_attn")
 
 
 def sfi_quant_poll_error(qkv) -> int:
@@ -440,9 +446,10 @@ def sfi_quant_poll_error(qkv) -> int:
 
 
 def sfi_block_build(shape, kv, index, pos_lo, L, lens=None, stream=None):
+    dev = torch.cuda.current_device()
     _dims(shape, index)
-    _check(lib().sfi_block_build(C.byref(shape), C.byref(kv), C.byref(index), pos_lo, L, _lens(shape, lens),
-                                 _on(stream)), "sfi_block_build")
+    _check(lib().sfi_block_build(C.byref(shape), C.byref(kv), C.byref(index), pos_lo, L, _lens(shape.B, lens, dev),
+                                 _on(stream, dev)), "sfi_block_build")
 
 
 def sfi_block_workspace_size(shape: Shape) -> int:
@@ -453,25 +460,30 @@ def sfi_block_workspace_size(shape: Shape) -> int:
 
 def sfi_block_select(shape, index, L, q, n_sink, n_recent, K, sel, ws, lens=None, stream=None):
     """sel: int32 [B, Hkv, at least K]."""
+    dev = torch.cuda.current_device()
     _dims(shape, index)
-    q = _arg(q, "q", _BF16, (shape.B, shape.Hq, shape.D))
-    _check(lib().sfi_block_select(C.byref(shape), C.byref(index), L, _lens(shape, lens), q, n_sink, n_recent, K,
-                                  _sel(shape, sel), sel.shape[-1], *_ws(ws), _on(stream)), "sfi_block_select")
+    _check(lib().sfi_block_select(C.byref(shape), C.byref(index), L, _lens(shape.B, lens, dev),
+                                  _arg(q, "q", _BF16, (shape.B, shape.Hq, shape.D), dev), n_sink, n_recent, K,
+                                  _sel(shape, sel, dev), sel.shape[-1], *_ws(ws, dev), _on(stream, dev)),
+           "sfi_block_select")
 
 
 def sfi_block_attn(shape, kv, L, q, sel, K, out, ws, lens=None, lse=None, stream=None):
     """Attention over blocks sel[:, :, :K] of the bf16 cache."""
-    q, out, lse = _attn_args(shape, q, out, lse)
-    _check(lib().sfi_block_attn(C.byref(shape), C.byref(kv), L, _lens(shape, lens), q, _sel(shape, sel),
-                                sel.shape[-1], K, out, lse, *_ws(ws), _on(stream)), "sfi_block_attn")
+    dev = torch.cuda.current_device()
+    q, out, lse = _attn_args(shape, q, out, lse, dev)
+    _check(lib().sfi_block_attn(C.byref(shape), C.byref(kv), L, _lens(shape.B, lens, dev), q, _sel(shape, sel, dev),
+                                sel.shape[-1], K, out, lse, *_ws(ws, dev), _on(stream, dev)), "sfi_block_attn")
 
 
 def sfi_quant_block_attn(shape, qkv, L, q, sel, K, out, ws, lens=None, lse=None, stream=None):
     """sfi_block_attn on the 8-bit cache."""
+    dev = torch.cuda.current_device()
     _dims(shape, qkv)
-    q, out, lse = _attn_args(shape, q, out, lse)
-    _check(lib().sfi_quant_block_attn(C.byref(shape), C.byref(qkv), L, _lens(shape, lens), q, _sel(shape, sel),
-                                      sel.shape[-1], K, out, lse, *_ws(ws), _on(stream)), "sfi_quant_block_attn")
+    q, out, lse = _attn_args(shape, q, out, lse, dev)
+    _check(lib().sfi_quant_block_attn(C.byref(shape), C.byref(qkv), L, _lens(shape.B, lens, dev), q,
+                                      _sel(shape, sel, dev), sel.shape[-1], K, out, lse, *_ws(ws, dev),
+                                      _on(stream, dev)), "sfi_quant_block_attn")
 
 
 class Context:
