@@ -357,8 +357,15 @@ sfi_status sfi_selftest_wait(const sfi_paged_kv* kv, int64_t limit_ns, sfi_strea
  *   scale = amax / Q,  code = round(x * (Q / amax)), ties to even,
  *   Q = 448 (SFI_FMT_E4M3) or 127 (SFI_FMT_INT8), all in fp32.
  * A page holding an infinity or a NaN stores a NaN scale (and codes 0): all of
- * it stands for NaN.  The NaN codes of e4m3 are never written and must not be
- * handed in.
+ * it stands for NaN.  The NaN codes of e4m3 are never written.
+ *
+ * The tail holds one page: a length may go back (a token appended again) within
+ * the page of the last append; further back, store the tokens again.
+ *
+ * Ordering.  The calls of this section and the next wait for all earlier work
+ * on their stream before they read or write.  For a later attention call of the
+ * sections above they are earlier attention calls: its early loads, and a fast
+ * call's append, may overlap them, under the rule given there.
  *
  * Lengths.  Every call below takes L and lens: with lens == NULL each sequence
  * has L tokens; else lens (device int32 [B]) gives each sequence's own, in
@@ -435,9 +442,8 @@ sfi_status sfi_quant_load(const sfi_shape* shape, const sfi_quant_kv* qkv, const
  *       (out 16-byte aligned)
  * An empty sequence gets out = 0 and lse = -infinity.  ws: scratch of
  * sfi_block_workspace_size bytes, 16-byte aligned, zero-filled before its first
- * use; every call leaves it ready for the next, of any of the four calls below
- * and any lengths of the same shape.  Calls that share one ws must not run
- * concurrently. */
+ * use; every call leaves it ready for the next one that takes it, of any shape
+ * whose size it has.  Calls that share one ws must not run concurrently. */
 sfi_status sfi_quant_attn(const sfi_shape* shape, const sfi_quant_kv* qkv, int32_t L, const int32_t* lens,
                           const sfi_bf16* q, float* out, float* lse, void* ws, size_t ws_bytes,
                           sfi_stream stream);

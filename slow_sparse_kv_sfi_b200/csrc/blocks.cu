@@ -491,11 +491,14 @@ cudaError_t launch_select(const SelectArgs& a, int BH, int cs, cudaStream_t st) 
 
 }  // namespace
 
+// The arrival counts come first and have one size: a workspace may then serve
+// layers of several shapes, each of which finds them zero.
 BlockWs block_ws(const sfi_shape& s) {
   BlockWs w{};
   const long long BH = (long long)s.B * s.Hkv;
   const int G = s.Hq / s.Hkv;
-  size_t off = 0;
+  w.arrived_off = 0;
+  size_t off = align_up((size_t)kMaxRows * sizeof(int), 256);
   w.score_off = off;
   off += align_up((size_t)BH * (((size_t)s.max_pages + 3) / 4 * 4) * sizeof(float), 256);
   const size_t items = 2 * (size_t)page_attn_ctas_bound(BH, s.max_pages);
@@ -503,8 +506,6 @@ BlockWs block_ws(const sfi_shape& s) {
   off += align_up(items * G * s.D * sizeof(float), 256);
   w.ml_off = off;
   off += align_up(items * G * 2 * sizeof(float), 256);
-  w.arrived_off = off;
-  off += align_up((size_t)BH * sizeof(int), 256);
   w.total = off;
   return w;
 }
@@ -533,7 +534,7 @@ sfi_status sfi_block_select(const sfi_shape* shape, const sfi_block_index* index
   const int nb = (L + kPage - 1) / kPage;
   const long always = ((long)n_sink + kPage - 1) / kPage + ((long)n_recent + kPage - 1) / kPage + 1;
   if (K < 1 || K > nb || K < (always < nb ? always : nb) || sel_ld < K) return SFI_ERR_SHAPE;
-  if (nb > topk_max_n() || (long)shape->B * shape->Hkv > 65535) return SFI_ERR_UNSUPPORTED;
+  if (nb > topk_max_n() || (long)shape->B * shape->Hkv > kMaxRows) return SFI_ERR_UNSUPPORTED;
   const BlockWs w = block_ws(*shape);
   if (!ws || !aligned16(ws) || ws_bytes < w.total) return SFI_ERR_WORKSPACE;
   const int BH = shape->B * shape->Hkv;

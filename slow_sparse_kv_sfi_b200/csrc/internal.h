@@ -199,10 +199,11 @@ int score_tile(int G);
 int stat_chunks(int nC);
 
 
-// Block-sparse and 8-bit calls: scratch is [scores][partials (O)][partials
-// (m, l)][arrival counts, zero between calls].
+// Block-sparse and 8-bit calls: scratch is [arrival counts, zero between
+// calls][scores][partials (O)][partials (m, l)].
+constexpr int kMaxRows = 65535;   // (sequence, KV head) pairs
 struct BlockWs {
-  size_t score_off, part_off, ml_off, arrived_off, total;
+  size_t arrived_off, score_off, part_off, ml_off, total;
 };
 BlockWs block_ws(const sfi_shape& s);
 // The most CTAs that a page attention launch has for `rows` (sequence, KV

@@ -990,7 +990,7 @@ sfi_status run(const sfi_shape* shape, const sfi_paged_kv* kv, const sfi_quant_k
     if (K > shape->max_pages) return SFI_ERR_SHAPE;
   }
   const long BHl = (long)shape->B * shape->Hkv;
-  if (BHl > 65535) return SFI_ERR_UNSUPPORTED;
+  if (BHl > kMaxRows) return SFI_ERR_UNSUPPORTED;
   const BlockWs w = block_ws(*shape);
   if (!ws || !aligned16(ws) || ws_bytes < w.total) return SFI_ERR_WORKSPACE;
   PageAttnArgs a{};

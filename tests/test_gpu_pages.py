@@ -10,8 +10,8 @@ P by twice that; the sums over tokens and warps add at most (tiles + 64) * 2^-23
 All of it relative to sum p |v|.  On the 8-bit cache P is fp16 (rounded twice, less
 than the bf16 term above), where besides a value below fp16's smallest step is lost:
 that step is 2^-24, P's largest value at least 2^8 and the sum of P at least that, so a
-weight P / sum P is off by at most half a step over 2^8, 2^-33, and an output by at most
-2^-33 sum |v| more.
+weight p = P / max P is off by at most half a step over 2^8, 2^-33, or by itself where it
+is smaller, and an output by at most sum min(2^-33, p) |v| more.
 """
 import math
 
@@ -107,7 +107,8 @@ def check_attn(got, lse, q, K, V, what):
         return
     dz = (D / 16 + 2) * 2.0 ** -23 * s + 2.0 ** -22 * np.abs(s)
     rel = 2.0 ** -16 + 2 * dz + (len(K) / 16 + 64) * 2.0 ** -23
-    tol = rel[:, None] * pv + 2.0 ** -33 * np.abs(V).sum(0) + 1e-30
+    z = q @ K.T / math.sqrt(D)
+    tol = rel[:, None] * pv + np.minimum(2.0 ** -33, np.exp(z - z.max(1, keepdims=True))) @ np.abs(V) + 1e-30
     assert np.all(np.abs(got - o) <= tol), (what, (np.abs(got - o) / tol).max())
     assert np.all(np.abs(lse - ref_lse) <= 2 * dz + (len(K) / 16 + 64) * 2.0 ** -23 + 2.0 ** -22 * np.abs(ref_lse)), what
 
@@ -690,3 +691,81 @@ def test_calls_stay_inside_their_workspace(B, Hq, Hkv, L):
     check_all(c, lambda b, h, n: c.quant_rows("k", b, h, n), lambda b, h, n: c.quant_rows("v", b, h, n))
     for o in outs[:-1]:   # all of them attend to everything; the cuts differ
         assert float((o - outs[-1]).abs().max()) <= 1e-5 * float(c.v.float().abs().max())
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("D,Hq", [(64, 3), (128, 6), (128, 13)])
+def test_value_scales_far_apart(fmt, D, Hq):
+    """Pages of values from 1e-25 to 1e30, the weight on small ones: pages 2^6 and more below the
+    largest scale so far, and scales that rise along the sequence."""
+    n = 20 * PAGE + 5
+    c = Case(1, Hq, 1, D, [n], fmt, seed=20)
+    unit = torch.zeros(D)
+    unit[0] = 1.0
+    amp = [1.0, 1e30, 1e-3, 1e25, 1e-25, 1.0, 1e28, 1e3] * 3
+    for j in range(21):
+        p = int(c.pt[0, j])
+        c.v[p] = (c.v[p].float() * amp[j]).to(torch.bfloat16)
+        # logits: high where the values are small, hundreds lower elsewhere
+        big = amp[j] >= 1e25
+        c.k[p, 0] = (c.k[p, 0].float() * 0.3 + unit * (-300.0 if big else 0.0)).to(torch.bfloat16)
+    c.q[0, :, 0] = 12.0
+    c.up()
+    S.sfi_quant_store(c.shape, c.kv, c.q8, 0, n)
+    S.sfi_quant_attn(c.shape, c.q8, n, c.qd, c.out, c.ws, lse=c.lse)
+    assert c.error() == 0
+    assert float(c.out.abs().max()) < 1e4
+    check_all(c, lambda b, h, m: c.quant_rows("k", b, h, m), lambda b, h, m: c.quant_rows("v", b, h, m))
+
+
+@pytest.mark.parametrize("Hq", [4, 8, 16])
+def test_nan_stays_where_it_is(Hq):
+    """A NaN in one head's query, and a page of values that is not finite."""
+    c = Case(2, Hq, 1, 64, [100, 70], "e4m3", seed=21)
+    c.q[0, 1, 3] = float("nan")
+    c.v[int(c.pt[1, 2]), 0, 4, 5] = float("inf")
+    c.up()
+    S.sfi_quant_store(c.shape, c.kv, c.q8, 0, c.L, lens=c.lend)
+    S.sfi_quant_attn(c.shape, c.q8, c.L, c.qd, c.out, c.ws, lens=c.lend, lse=c.lse)
+    assert c.error() == 0
+    assert torch.isnan(c.out[0, 1]).all() and torch.isnan(c.lse[0, 1])
+    assert torch.isnan(c.out[1]).all() and torch.isfinite(c.lse[1]).all()
+    K, V = c.quant_rows("k", 0, 0, 100), c.quant_rows("v", 0, 0, 100)
+    out, lse, q = c.out.cpu().double().numpy(), c.lse.cpu().double().numpy(), c.q.double().numpy()
+    rest = [h for h in range(Hq) if h != 1]
+    check_attn(out[0, rest], lse[0, rest], q[0, rest], K, V, "the other heads")
+
+
+def test_one_workspace_serves_several_shapes():
+    cases = [Case(1, 8, 2, 128, [3000], "e4m3", seed=22).up(), Case(5, 16, 8, 64, [700, 0, 33, 650, 16], "int8", seed=23).up(),
+             Case(1, 16, 1, 128, [5000], "int8", seed=24).up()]
+    ws = torch.zeros(max(c.ws.numel() for c in cases), dtype=torch.uint8, device=DEV)
+    for _ in range(2):
+        for c in cases:
+            c.out.fill_(float("nan"))
+            S.sfi_quant_store(c.shape, c.kv, c.q8, 0, c.L, lens=c.lend)
+            S.sfi_quant_attn(c.shape, c.q8, c.L, c.qd, c.out, ws, lens=c.lend, lse=c.lse)
+            assert c.error() == 0
+            check_all(c, lambda b, h, n: c.quant_rows("k", b, h, n), lambda b, h, n: c.quant_rows("v", b, h, n))
+
+
+def test_length_goes_back_within_the_page():
+    """Tokens appended, dropped and appended again inside the page, over its end included."""
+    c = Case(1, 2, 2, 64, [32], "int8", seed=25).up()
+    tok = lambda t, d: (c.k[c.pt[0, t // PAGE].long(), :, t % PAGE] * d)[None].to(DEV).contiguous()  # noqa: E731
+    for t in range(16):
+        S.sfi_quant_append(c.shape, c.q8, t + 1, tok(t, 2.0), tok(t, 2.0))
+    for t in range(11, 16):                       # back to 11 tokens, on with others
+        S.sfi_quant_append(c.shape, c.q8, t + 1, tok(t, 1.0), tok(t, 1.0))
+    assert c.error() == 0
+    p = int(c.pt[0, 0])
+    want = c.k[p].float().clone()
+    want[:, :11] *= 2
+    for h in range(2):
+        x = want[h].double().numpy()
+        y = P.code_values(c.kc[p, h].cpu().numpy(), "int8") * float(c.ks[p, h])
+        assert np.all(np.abs(y - x) <= P.half_step(x, P.page_scale(x, "int8"), "int8") * (1 + 2.0 ** -20) + 2.0 ** -20 * np.abs(x))
+    S.sfi_quant_attn(c.shape, c.q8, 13, c.qd, c.out, c.ws, lse=c.lse)     # 13 tokens: the tail's rows
+    torch.cuda.synchronize()
+    rows = lambda b, h, n: want[h, :13].to(torch.bfloat16).double().numpy()  # noqa: E731
+    check_all(c, rows, rows, [13])
