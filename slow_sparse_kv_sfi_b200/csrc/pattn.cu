@@ -800,9 +800,10 @@ __device__ __forceinline__ void attend_row(const PageAttnArgs& a, uint8_t* smem,
   __syncthreads();   // the piece is written
   int* last = reinterpret_cast<int*>(sml);   // the warps' (m, l) are used up
   if (threadIdx.x == 0) {
-    __threadfence();   // the CTA's piece before the count
-    const bool all = atomicAdd(a.arrived + bh, 1) == c1 - c0;
-    __threadfence();   // the count before the others' pieces
+    // releases the CTA's piece (written before the barrier), acquires the others'
+    int before;
+    asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(before) : "l"(a.arrived + bh) : "memory");
+    const bool all = before == c1 - c0;
     if (all) a.arrived[bh] = 0;   // for the next call
     *last = all;
   }

@@ -190,8 +190,8 @@ def make_packed(k, v, pos, headmask, n_rows) -> Packed:
 def _arg(t, name, dtypes, shape=None, dev=None):
     """Checks a tensor argument of the 8-bit and block calls (dev: the current device, where known) and
     returns its address."""
-    if (t.dtype in dtypes and (shape is None or t.shape == shape) and t.is_contiguous()
-            and t.is_cuda and t.get_device() == (torch.cuda.current_device() if dev is None else dev)):
+    if (t.dtype in dtypes and (shape is None or t.shape == shape) and t.is_contiguous() and t.is_cuda
+            and t.get_device() == (torch.cuda.current_device() if dev is None else dev)):
         return t.data_ptr()
     if t.dtype not in dtypes:
         raise ValueError(f"{name}: dtype {t.dtype}, expected {' or '.join(str(d) for d in dtypes)}")
@@ -274,7 +274,7 @@ def _sel(shape, sel, dev):
 
 
 def _ws(ws, dev):
-    return _arg(ws, "ws", (ws.dtype,), None, dev), ws.numel() * ws.element_size()
+    return _arg(ws, "ws", (ws.dtype,), None, dev), ws.nbytes
 
 
 # ---------------------------------------------------------------- entry points
