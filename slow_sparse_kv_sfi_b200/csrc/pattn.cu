@@ -9,8 +9,9 @@
 // (a row counts for some tiles more than it has, see Cfg::kRowCost); the grid is
 // what the GPU holds at once.  Rows of one length that divide well get the same
 // number of CTAs each instead, see launch().  A run cuts at most two rows: a row
-// inside one run is finished there, the pieces of the others are merged by the
-// CTA that writes the last of them, in the order of the pieces, whoever that is.
+// inside one run is finished there; the pieces of the others are merged by the
+// CTA that writes the last of them, in an order that is the same whoever that is,
+// or, where that would be much work for one CTA, by a second kernel.
 // Within a row, warp w of the CTA takes tiles w, w + W, ...; each warp runs its
 // own online softmax and the CTA merges its warps in shared memory.
 //
@@ -71,6 +72,8 @@ struct PageAttnArgs {
   int total;                        // units of all rows (row_units), or -1: by lens
   int quota;                        // units of a CTA's run (total >= 0)
   int row_cost;                     // units of a row besides its tiles
+  int ctas;                         // of the grid
+  int merge_later;                  // pieces are merged by the next kernel
   int pieces;                       // > 0: CTAs of each row, whose runs begin with the row; 0: even runs
   float scale_log2;                 // log2(e) / sqrt(D)
   float* out;
@@ -442,6 +445,17 @@ __device__ __forceinline__ void write_out(const PageAttnArgs& a, size_t row, int
 
 constexpr int kMaxGroups = 8;
 
+// The CTAs with a piece of a row: its first unit is row0, its tiles T > 0.
+__device__ __forceinline__ void row_ctas(const PageAttnArgs& a, int b, int h, int T, int row0, int run, int& c0, int& c1) {
+  if (a.pieces > 0) {
+    c0 = (b * a.Hkv + h) * a.pieces;
+    c1 = c0 + a.pieces - 1;
+  } else {
+    c0 = (int)((unsigned)(row0 + a.row_cost) / (unsigned)run);
+    c1 = (int)((unsigned)(row0 + T + a.row_cost - 1) / (unsigned)run);
+  }
+}
+
 // Tiles [t0, t1) of the T tiles of row (b, h), by the whole CTA: the row's
 // output, or (not the whole row) its piece, and the output too if that is the
 // last.  c0, c1: the first and last CTA with a piece of the row.
@@ -796,6 +810,8 @@ __device__ __forceinline__ void attend_row(const PageAttnArgs& a, uint8_t* smem,
   }
   if (whole) return;
 
+  if (a.merge_later) return;
+
   // The CTA that writes a row's last piece merges them all.
   __syncthreads();   // the piece is written
   int* last = reinterpret_cast<int*>(sml);   // the warps' (m, l) are used up
@@ -869,7 +885,7 @@ __global__ void __launch_bounds__(Cfg<D, FMT, HM>::W * 32, Cfg<D, FMT, HM>::kCta
     left = min(run, T + a.row_cost - v0);
   } else {
     const int total = count_units(a, lane, warp == 0 ? a.err : nullptr);
-    run = a.total >= 0 ? a.quota : quota(total, gridDim.x, a.row_cost);
+    run = a.total >= 0 ? a.quota : quota(total, a.ctas, a.row_cost);
     const int pos = (int)min((long long)run * blockIdx.x, (long long)total);
     left = min(run, total - pos);
     if (left > 0) {
@@ -890,13 +906,7 @@ __global__ void __launch_bounds__(Cfg<D, FMT, HM>::W * 32, Cfg<D, FMT, HM>::kCta
       const int v1 = min(V, v0 + left);
       if (v1 > a.row_cost) {   // else none of its tiles
         int c0, c1;
-        if (a.pieces > 0) {
-          c0 = (b * a.Hkv + h) * a.pieces;
-          c1 = c0 + a.pieces - 1;
-        } else {
-          c0 = (int)((unsigned)(row0 + a.row_cost) / (unsigned)run);
-          c1 = (int)((unsigned)(row0 + V - 1) / (unsigned)run);
-        }
+        row_ctas(a, b, h, T, row0, run, c0, c1);
         attend_row<D, FMT, HM, LIST>(a, smem, b, h, len, T, max(0, v0 - a.row_cost), v1 - a.row_cost, c0, c1);
         __syncthreads();   // the row's shared memory is free
       }
@@ -912,6 +922,76 @@ __global__ void __launch_bounds__(Cfg<D, FMT, HM>::W * 32, Cfg<D, FMT, HM>::kCta
         write_out<D>(a, (size_t)i * a.Hq + e / (D / 4), e % (D / 4) * 4, 0.f, 0.f, make_float4(0.f, 0.f, 0.f, 0.f));
     }
   }
+}
+
+// Merge of the pieces of rows, a CTA per query head.  The pieces' (m, l) come in
+// first, all at once; then each thread adds up four columns over its share of the
+// pieces, in an order that the sizes alone give, and no load waits for another.
+constexpr int kMergeThreads = 256;
+constexpr int merge_smem(int pieces) { return kMergeThreads * 16 + pieces * 8 + 64; }   // acc, ml, group_l
+
+template <int D, bool LIST>
+__global__ void __launch_bounds__(kMergeThreads) page_merge_kernel(const __grid_constant__ PageAttnArgs a) {
+  grid_dep_enter();
+  extern __shared__ __align__(16) float merge_sm[];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int head = blockIdx.x, b = head / a.Hq, hq = head - b * a.Hq, h = hq / a.G, n = hq - h * a.G;
+  const int T = row_tiles<LIST>(a, b, nullptr);
+  if (T == 0) return;   // written by the attention kernel, as are rows in one piece
+  int row0 = 0, run = a.quota;
+  if (a.pieces == 0) {
+    const int V = row_units(T, a.row_cost);
+    if (a.total >= 0) {
+      row0 = (b * a.Hkv + h) * V;
+    } else {
+      int before = 0, all = 0;
+      for (int i = lane; i < a.B; i += 32) {
+        const int u = row_units(row_tiles<LIST>(a, i, nullptr), a.row_cost);
+        all += u;
+        if (i < b) before += u;
+      }
+      row0 = (int)__reduce_add_sync(0xffffffffu, (unsigned)before) * a.Hkv + h * V;
+      run = quota((int)__reduce_add_sync(0xffffffffu, (unsigned)all) * a.Hkv, a.ctas, a.row_cost);
+    }
+  }
+  int c0, c1;
+  row_ctas(a, b, h, T, row0, run, c0, c1);
+  if (c0 == c1) return;
+  const int P = c1 - c0 + 1;
+  float4* acc = reinterpret_cast<float4*>(merge_sm);               // [groups][D / 4]
+  float2* ml = reinterpret_cast<float2*>(acc + kMergeThreads);     // [P] (m, l)
+  __shared__ float2 warp_ml[kMergeThreads / 32];
+  // only the first piece begins inside its CTA's run
+  auto at = [&](int c) { return ((size_t)(c0 + c) * 2 + (c > 0 ? 0 : 1)) * a.G + n; };
+  float M = kNoMax;
+  for (int c = tid; c < P; c += kMergeThreads) {
+    ml[c] = __ldcg(reinterpret_cast<const float2*>(a.ml + at(c) * 2));
+    M = fmaxf(M, ml[c].x);
+  }
+#pragma unroll
+  for (int sh = 16; sh >= 1; sh >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, sh));
+  if (lane == 0) warp_ml[warp].x = M;
+  __syncthreads();
+  for (int w = 0; w < kMergeThreads / 32; ++w) M = fmaxf(M, warp_ml[w].x);
+  constexpr int kSlots = D / 4, kGroups = kMergeThreads / kSlots;
+  const int grp = tid / kSlots, slot = tid % kSlots;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  float l = 0.f;   // of this group's pieces
+#pragma unroll 8
+  for (int c = grp; c < P; c += kGroups) {
+    const float f = fast_exp2(ml[c].x - M);
+    l += f * ml[c].y;
+    add_scaled(o, f, __ldcg(reinterpret_cast<const float4*>(a.part + at(c) * D + slot * 4)));
+  }
+  acc[tid] = o;
+  float* group_l = reinterpret_cast<float*>(ml + P);
+  if (slot == 0) group_l[grp] = l;
+  __syncthreads();
+  if (tid >= kSlots) return;
+  for (int i = 1; i < kGroups; ++i) add_scaled(o, 1.f, acc[i * kSlots + slot]);
+  l = 0.f;
+  for (int i = 0; i < kGroups; ++i) l += group_l[i];
+  write_out<D>(a, (size_t)b * a.Hq + hq, slot * 4, M, l, o);
 }
 
 #define SFI_TRY(x)               \
@@ -958,7 +1038,20 @@ sfi_status launch(PageAttnArgs& a, cudaStream_t st) {
       ctas = rows * a.pieces;
     }
   }
-  return cuda_status(launch_k(k, dim3(ctas), dim3(C::W * 32), C::kSmem, st, a));
+  a.ctas = ctas;
+  // A row in many pieces is merged by a kernel with a CTA per head, which costs
+  // a launch (about as much as 16 loads in a row), instead of by its last CTA: by
+  // the loads that a thread of each has in a row.  Of ragged lengths the longest
+  // may have several times the average's pieces.  us, last CTA against kernel, at
+  // rows x heads of a row, e4m3: 57K 4x16 73.7, 29.5; 57K 4x8 30.9, 22.2; 4K 8x16
+  // 18.8, 12.6; 64K ragged 32x16 86.0, 74.4; the other way 8K 64x4 21.0, 21.7;
+  // 128K 16x4 88.4, 89.1; 32K 32x8 51.2, 51.5; 100K 1x1 15.9, 19.3.  (Wrong for
+  // 64K ragged 32x4 int8, to the kernel: 48.1, 49.5.)
+  const int pieces = a.pieces > 0 ? a.pieces : ((ctas + rows - 1) / rows + 1) * (a.total < 0 ? 4 : 1);
+  a.merge_later = pieces * a.G * (D / 4) / (C::W * 32) > pieces * (D / 4) / kMergeThreads + 16;
+  const sfi_status r = cuda_status(launch_k(k, dim3(ctas), dim3(C::W * 32), C::kSmem, st, a));
+  if (r != SFI_OK || !a.merge_later) return r;
+  return cuda_status(launch_k(page_merge_kernel<D, LIST>, dim3(a.B * a.Hq), dim3(kMergeThreads), merge_smem(ctas), st, a));
 }
 
 template <int D, int FMT, bool LIST>

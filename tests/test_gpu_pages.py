@@ -718,6 +718,45 @@ def test_value_scales_far_apart(fmt, D, Hq):
     check_all(c, lambda b, h, m: c.quant_rows("k", b, h, m), lambda b, h, m: c.quant_rows("v", b, h, m))
 
 
+@pytest.mark.parametrize("B,Hq,Hkv,D,lens", [
+    (1, 16, 1, 64, [9001]), (1, 64, 4, 128, [6000]), (3, 32, 2, 128, [4097, 0, 65]), (2, 24, 2, 64, [9000, 1]),
+    (2, 32, 2, 64, [5000, 5000]), (40, 16, 1, 64, [7000] + [1] * 38 + [300])])
+def test_rows_in_many_pieces(B, Hq, Hkv, D, lens):
+    """Few rows of many heads: of one length, of very uneven ones, and as lists of blocks; a NaN in
+    one head's query stays there; a second call gives the same bits."""
+    c = Case(B, Hq, Hkv, D, lens, "int8", seed=22)
+    c.q[0, Hq // Hkv - 2, 3] = float("nan")
+    c.up()
+    S.sfi_quant_store(c.shape, c.kv, c.q8, 0, c.L, lens=c.lend)
+    nb = -(-c.L // PAGE)
+    sel = torch.arange(nb, dtype=torch.int32).flip(0).expand(B, Hkv, nb).contiguous().to(DEV)
+    calls = [lambda n: S.sfi_quant_attn(c.shape, c.q8, c.L, c.qd, c.out, c.ws, lens=n, lse=c.lse),
+             lambda n: S.sfi_quant_block_attn(c.shape, c.q8, c.L, c.qd, sel, nb, c.out, c.ws, lens=n, lse=c.lse)]
+    K, V = {}, {}
+    for b, n in enumerate(lens):
+        for h in range(Hkv):
+            K[b, h], V[b, h] = c.quant_rows("k", b, h, n), c.quant_rows("v", b, h, n)
+    for call in calls:
+        for n in (c.lend, None) if min(lens) == c.L else (c.lend,):
+            got = []
+            for _ in range(2):
+                c.out.fill_(float("nan"))
+                c.lse.fill_(float("nan"))
+                call(n)
+                assert c.error() == 0
+                got.append((c.out.clone(), c.lse.clone()))
+            bits = [[x.view(torch.int32) for x in g] for g in got]
+            assert all(torch.equal(x, y) for x, y in zip(*bits))
+            bad = Hq // Hkv - 2
+            assert torch.isnan(c.out[0, bad]).all() and torch.isnan(c.lse[0, bad])
+            out, lse, q = c.out.cpu().double().numpy(), c.lse.cpu().double().numpy(), c.q.double().numpy()
+            for b in range(B):
+                for h in range(Hkv):
+                    G = Hq // Hkv
+                    hs = [x for x in range(h * G, h * G + G) if (b, x) != (0, bad)]
+                    check_attn(out[b, hs], lse[b, hs], q[b, hs], K[b, h], V[b, h], (b, h))
+
+
 @pytest.mark.parametrize("Hq", [4, 8, 16])
 def test_nan_stays_where_it_is(Hq):
     """A NaN in one head's query, and a page of values that is not finite."""
