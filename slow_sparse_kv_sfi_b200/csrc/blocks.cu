@@ -16,6 +16,9 @@
 // the 16-byte chunks t, t + 4, ... of its two rows.
 #include <cooperative_groups.h>
 
+#include <algorithm>
+#include <atomic>
+
 #include "common.cuh"
 #include "internal.h"
 
@@ -457,28 +460,48 @@ __global__ void __launch_bounds__(kThreads, 1) block_select_kernel(const SelectA
   for (uint32_t m = ma | me; m; m &= m - 1) out[at++] = i0 + lane * 32 + __ffs(m) - 1;
 }
 
+// A cluster per row: the largest that lets all rows run at once and leaves every
+// warp a tile.  A cluster lies inside a GPC, whose multiprocessors it may not
+// use up, so the device says how many it holds (one CTA per multiprocessor: 15
+// clusters of 7 or 8, 22 of 6, 26 of 5, 33 of 4, 45 of 3, 74 of 2).  us for rows
+// of 8193 blocks, clusters of 4, 6, 8: 15 rows 21.5, 18.6, 16.5; 16 rows 22.1,
+// 19.1, 24.6; 24 rows 23.9, 32.3, 28.0.
 template <int D, int NT>
-cudaError_t launch_select(const SelectArgs& a, int BH, int cs, cudaStream_t st) {
-  const size_t smem = (size_t)((a.nb + 3) / 4 * 4) * sizeof(uint32_t);
+cudaError_t launch_select(const SelectArgs& a, int BH, cudaStream_t st) {
   auto k = block_select_kernel<D, NT>;
   static DeviceOnce once;
-  if (!once.done()) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxRow * (int)sizeof(uint32_t));
-    if (!once.mark(e)) return e;
-  }
+  static std::atomic<int> room[64][kMaxCluster + 1];   // by device and cluster size
+  int dev = 0;
+  cudaGetDevice(&dev);
+  dev &= 63;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(BH * cs);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = cs;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
+  if (!once.done()) {
+    cudaError_t e =
+        cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxRow * (int)sizeof(uint32_t));
+    cfg.dynamicSmemBytes = kMaxRow * sizeof(uint32_t);
+    cfg.numAttrs = 2;
+    for (int cs = 1; cs <= kMaxCluster && e == cudaSuccess; ++cs) {
+      cfg.gridDim = dim3(cs);
+      attr[1].val.clusterDim.x = cs;
+      int n = 0;
+      e = cudaOccupancyMaxActiveClusters(&n, k, &cfg);
+      room[dev][cs].store(n);
+    }
+    if (!once.mark(e)) return e;
+  }
+  int cs = std::min(kMaxCluster, (a.nb + kWarps * 16 - 1) / (kWarps * 16));
+  while (cs > 1 && BH > room[dev][cs].load()) --cs;
+  cfg.gridDim = dim3(BH * cs);
+  cfg.dynamicSmemBytes = (size_t)((a.nb + 3) / 4 * 4) * sizeof(uint32_t);
+  cfg.stream = st;
+  attr[1].val.clusterDim.x = cs;
   cfg.numAttrs = cs > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, k, a);
 }
@@ -564,12 +587,8 @@ sfi_status sfi_block_select(const sfi_shape* shape, const sfi_block_index* index
   const bool wide = a.G > 8;
   cudaError_t e;
   if (nb <= kMaxRow) {
-    // one launch: a cluster per row, as many CTAs as fit one each multiprocessor
-    // and leave every warp a tile
-    int cs = 1;
-    while (cs < kMaxCluster && 2L * cs * BH <= num_sms() && cs * kWarps * 16 < nb) cs *= 2;
-    e = shape->D == 128 ? (wide ? launch_select<128, 2>(a, BH, cs, st) : launch_select<128, 1>(a, BH, cs, st))
-                        : (wide ? launch_select<64, 2>(a, BH, cs, st) : launch_select<64, 1>(a, BH, cs, st));
+    e = shape->D == 128 ? (wide ? launch_select<128, 2>(a, BH, st) : launch_select<128, 1>(a, BH, st))
+                        : (wide ? launch_select<64, 2>(a, BH, st) : launch_select<64, 1>(a, BH, st));
   } else {
     const int tiles = (nb + 15) / 16;
     int gx = (tiles + kWarps - 1) / kWarps;

@@ -404,6 +404,23 @@ def test_select(B, Hq, Hkv, D, lens, n_sink, n_recent, K):
     assert (sel[..., K:] == -7).all()
 
 
+@pytest.mark.parametrize("rows", [3, 15, 16, 23, 27, 34, 46, 75, 149])
+def test_select_rows_at_once(rows):
+    """Row counts around those at which a row gets fewer of the GPU's multiprocessors."""
+    n = 16 * 16 * 8 * 2 + 5   # blocks for every warp of the largest cluster, and some for a second one
+    c = Case(1, rows, rows, 64, [n * PAGE - 3] if rows < 20 else [700 * PAGE + 1], seed=23, slack=1).up()
+    S.sfi_block_build(c.shape, c.kv, c.ix, 0, c.L)
+    sel = torch.full((1, rows, 40), -7, dtype=torch.int32, device=DEV)
+    S.sfi_block_select(c.shape, c.ix, c.L, c.qd, 4, 64, 40, sel, c.ws)
+    assert c.error() == 0
+    b, s, pt = c.bounds.cpu().numpy(), c.bscale.cpu().double().numpy(), c.pt[0].numpy()
+    nb = -(-c.L // PAGE)
+    q = c.q[0].double().numpy()
+    for h in range(rows):
+        u = P.block_scores(q[h:h + 1], b[pt[:nb], h].astype(np.int64), s[pt[:nb], h])
+        assert np.array_equal(sel[0, h].cpu().numpy(), P.select(u, c.L, 4, 64, 40)), h
+
+
 def test_select_ties_zeros_and_extreme_queries():
     """Equal pages (ties to the lower block), a zero query, and queries of 1e38, 1e-38, NaN and infinity."""
     c = Case(1, 6, 1, 64, [800], seed=11)
