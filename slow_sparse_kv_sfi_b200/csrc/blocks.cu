@@ -185,14 +185,15 @@ __device__ __forceinline__ void score_tiles(const SelectArgs& a, int h, const Wh
 }
 
 // Scores of the blocks below n of row (b, h), two tiles at a time, by warp
-// `first` of `warps`: put(block, score).
-template <int D, int NT, class Put>
+// `first` of `warps`: put(block, score).  ready() brings the query into s.
+template <int D, int NT, class Ready, class Put>
 __device__ __forceinline__ void score_row(const SelectArgs& a, int b, int h, int len, int n, int first, int warps,
-                                          int lane, const Query<D, NT>& s, Put put) {
+                                          int lane, const Query<D, NT>& s, Ready ready, Put put) {
   constexpr int U = 2;
   Where w[U];
 #pragma unroll
   for (int i = 0; i < U; ++i) w[i] = locate(a, b, len, first + i * warps, lane);
+  ready();
   for (int tile = first; tile * 16 < n; tile += U * warps) {
     Where next[U];
 #pragma unroll
@@ -215,11 +216,10 @@ __global__ void __launch_bounds__(kThreads, 1) block_score_kernel(const SelectAr
   __shared__ Query<D, NT> s;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int bh = blockIdx.y, b = bh / a.Hkv, h = bh - b * a.Hkv;
-  load_query<D, NT>(a, b, h, s);
   const int len = seq_len(a.lens, a.L, b, a.err);
   float* row = a.scores + (size_t)bh * a.ld;
   score_row<D, NT>(a, b, h, len, a.nb, blockIdx.x * kWarps + warp, gridDim.x * kWarps, lane, s,
-                   [&](int j, float u) { row[j] = u; });
+                   [&]() { load_query<D, NT>(a, b, h, s); }, [&](int j, float u) { row[j] = u; });
 }
 
 // A key back to its score (the inverse of float_key).
@@ -264,15 +264,11 @@ __device__ __forceinline__ uint32_t kth_key(const uint32_t* keys, int n, int K, 
   for (int i = 0; i < 4; ++i) s.hist[i * kThreads + threadIdx.x] = 0;
   if (threadIdx.x == 0) s.m = 0;
   __syncthreads();
-  uint32_t lo = kForced, hi = 0u;
-  forced = 0u;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    const uint4 v = *reinterpret_cast<const uint4*>(s.cnt[0][w]);
-    lo = min(lo, v.x);
-    hi = max(hi, v.y);
-    forced += v.z;
-  }
+  // (lane w takes warp w's: kWarps reads by every lane took 500 cycles more)
+  const uint4 v = lane < kWarps ? *reinterpret_cast<const uint4*>(s.cnt[0][lane]) : make_uint4(kForced, 0u, 0u, 0u);
+  uint32_t lo = __reduce_min_sync(0xffffffffu, v.x);
+  uint32_t hi = __reduce_max_sync(0xffffffffu, v.y);
+  forced = __reduce_add_sync(0xffffffffu, v.z);
   const int need = K - (int)forced;
   if (need <= 0) return kForced - 1u;   // the forced ones are all
   // monotone in the score; a range that overflows puts all into one bin, and
@@ -301,9 +297,7 @@ __device__ __forceinline__ uint32_t kth_key(const uint32_t* keys, int n, int K, 
   }
   if (lane == 31) s.scan[warp] = x;
   __syncthreads();
-  int above = x - sum;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) above += w < warp ? s.scan[w] : 0;
+  int above = x - sum + (int)__reduce_add_sync(0xffffffffu, lane < warp ? (unsigned)s.scan[lane] : 0u);
   if (above < need && above + sum >= need) {   // one thread
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -358,14 +352,10 @@ __device__ __forceinline__ uint32_t kth_key(const uint32_t* keys, int n, int K, 
     c2 = __reduce_add_sync(0xffffffffu, c2);
     if (lane == 0) *reinterpret_cast<uint4*>(s.cnt[round & 1][warp]) = make_uint4(c0, c1, c2, 0u);
     __syncthreads();   // the readers of this buffer's last use are past the last round's barrier
-    c0 = c1 = c2 = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const uint4 v = *reinterpret_cast<const uint4*>(s.cnt[round & 1][w]);
-      c0 += v.x;
-      c1 += v.y;
-      c2 += v.z;
-    }
+    const uint4 w = lane < kWarps ? *reinterpret_cast<const uint4*>(s.cnt[round & 1][lane]) : make_uint4(0u, 0u, 0u, 0u);
+    c0 = __reduce_add_sync(0xffffffffu, w.x);
+    c1 = __reduce_add_sync(0xffffffffu, w.y);
+    c2 = __reduce_add_sync(0xffffffffu, w.z);
     uint32_t c;
     if (c2 >= (uint32_t)K) {
       lo = m2;
@@ -392,9 +382,10 @@ __device__ __forceinline__ uint32_t kth_key(const uint32_t* keys, int n, int K, 
 // finds the K-th largest key and writes the chosen blocks in order.
 template <int D, int NT>
 __global__ void __launch_bounds__(kThreads, 1) block_select_kernel(const SelectArgs a) {
-  grid_dep_enter();
   namespace cg = cooperative_groups;
   cg::cluster_group cl = cg::this_cluster();
+  cl.barrier_arrive();   // this CTA runs, so its shared memory may be written
+  grid_dep_enter();
   extern __shared__ __align__(16) uint32_t keys[];   // of the cluster's first CTA
   __shared__ union Shared {
     Query<D, NT> query;
@@ -409,12 +400,15 @@ __global__ void __launch_bounds__(kThreads, 1) block_select_kernel(const SelectA
   if (n <= a.K) {   // the same in every CTA of the cluster
     if (rank == 0)
       for (int i = threadIdx.x; i < a.K; i += kThreads) out[i] = i;
+    cl.barrier_wait();
     return;
   }
-  load_query<D, NT>(a, b, h, sh.query);
   uint32_t* first = cl.map_shared_rank(keys, 0);
-  cl.sync();   // the first CTA runs, so its shared memory may be written
   score_row<D, NT>(a, b, h, len, n, rank * kWarps + warp, cs * kWarps, lane, sh.query,
+                   [&]() {
+                     load_query<D, NT>(a, b, h, sh.query);
+                     cl.barrier_wait();
+                   },
                    [&](int j, float u) { first[j] = u == INFINITY ? kForced : float_key(u); });
   cl.sync();
   if (rank != 0) return;
@@ -448,12 +442,9 @@ __global__ void __launch_bounds__(kThreads, 1) block_select_kernel(const SelectA
   }
   if (lane == 31) scan[warp] = x;
   __syncthreads();
-  int total = 0, before = x - own;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    total += scan[w] & 0xffff;
-    before += w < warp ? scan[w] : 0;
-  }
+  const unsigned of = lane < kWarps ? (unsigned)scan[lane] : 0u;
+  const int total = (int)__reduce_add_sync(0xffffffffu, of & 0xffffu);
+  const int before = x - own + (int)__reduce_add_sync(0xffffffffu, lane < warp ? of : 0u);
   const int take = a.K - total, eq = before >> 16;   // equal ones to take, and those in front of this lane's
   int at = (before & 0xffff) + min(eq, take);
   for (int drop = __popc(me) - max(take - eq, 0); drop > 0; --drop) me &= ~(0x80000000u >> __clz(me));
