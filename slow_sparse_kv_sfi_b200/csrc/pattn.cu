@@ -831,16 +831,28 @@ __device__ __forceinline__ void attend_row(const PageAttnArgs& a, uint8_t* smem,
     const int grp = e / slots, slot = e % slots, n_ = slot / (D / 4), d = slot % (D / 4) * 4;
     float M = kNoMax, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int c = c0 + grp; c <= c1; c += groups) {
-      const size_t r = ((size_t)c * 2 + (c > c0 ? 0 : 1)) * a.G + n_;   // only the first piece begins inside its run
-      const float2 ml = __ldcg(reinterpret_cast<const float2*>(a.ml + r * 2));
-      const float4 x = __ldcg(reinterpret_cast<const float4*>(a.part + r * D + d));
-      const float mn = fmaxf(M, ml.x);
-      const float f0 = fast_exp2(M - mn), f1 = fast_exp2(ml.x - mn);
-      l = l * f0 + ml.y * f1;
-      o = make_float4(o.x * f0, o.y * f0, o.z * f0, o.w * f0);
-      add_scaled(o, f1, x);
+    // four pieces' loads at a time, the last ones' too: one wait (us at 8K e4m3
+    // with the last ones in turn and this: 21.0, 20.3)
+    for (int c = c0 + grp; c <= c1; c += 4 * groups) {
+      float2 ml[4];
+      float4 x[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int ci = c + i * groups;
+        const size_t r = ((size_t)ci * 2 + (ci > c0 ? 0 : 1)) * a.G + n_;   // only the first piece begins inside its run
+        ml[i] = ci <= c1 ? __ldcg(reinterpret_cast<const float2*>(a.ml + r * 2)) : make_float2(kNoMax, 0.f);
+        x[i] = ci <= c1 ? __ldcg(reinterpret_cast<const float4*>(a.part + r * D + d)) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      const float mn = fmaxf(fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), M);
+      const float f = fast_exp2(M - mn);
+      l *= f;
+      o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float fi = fast_exp2(ml[i].x - mn);
+        l += ml[i].y * fi;
+        add_scaled(o, fi, x[i]);
+      }
       M = mn;
     }
     if (groups == 1) {
