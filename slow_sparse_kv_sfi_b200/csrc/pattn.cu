@@ -1054,15 +1054,16 @@ sfi_status launch(PageAttnArgs& a, cudaStream_t st) {
   }
   a.ctas = ctas;
   // A row in many pieces is merged by a kernel with a CTA per head, which costs
-  // a launch (about as much as 16 loads in a row), instead of by its last CTA: by
-  // the loads that a thread of each has in a row.  Of ragged lengths the longest
-  // may have several times the average's pieces.  us, last CTA against kernel, at
-  // rows x heads of a row, e4m3: 57K 4x16 73.7, 29.5; 57K 4x8 30.9, 22.2; 4K 8x16
-  // 18.8, 12.6; 64K ragged 32x16 86.0, 74.4; the other way 8K 64x4 21.0, 21.7;
-  // 128K 16x4 88.4, 89.1; 32K 32x8 51.2, 51.5; 100K 1x1 15.9, 19.3.  (Wrong for
-  // 64K ragged 32x4 int8, to the kernel: 48.1, 49.5.)
-  const int pieces = a.pieces > 0 ? a.pieces : ((ctas + rows - 1) / rows + 1) * (a.total < 0 ? 4 : 1);
-  a.merge_later = pieces * a.G * (D / 4) / (C::W * 32) > pieces * (D / 4) / kMergeThreads + 16;
+  // a launch (about as much as 16 loads in a row) and 4 more a wave of its CTAs, 8
+  // to a multiprocessor, instead of by its last CTA: by the loads that a thread of
+  // each has in a row.  us, last CTA against kernel, at rows x heads of a row,
+  // e4m3: 57K 4x16 73.7, 29.5; 57K 4x8 30.9, 22.2; 4K 8x16 18.8, 12.6; 64K ragged
+  // 32x16 86.0, 74.4; 8K ragged 64x16 35.2, 32.8; the other way 4K ragged 128x16
+  // 33.3, 36.0; 2K ragged 400x16 47.8, 66.6; 8K 64x4 21.0, 21.7; 128K 16x4 88.4,
+  // 89.1; 32K 32x8 51.2, 51.5; 100K 1x1 15.9, 19.3.
+  const int pieces = a.pieces > 0 ? a.pieces : (ctas + rows - 1) / rows + 1;
+  a.merge_later = pieces * a.G * (D / 4) / (C::W * 32) >
+                  pieces * (D / 4) / kMergeThreads + 16 + 4LL * a.B * a.Hq / (num_sms() * 8);
   const sfi_status r = cuda_status(launch_k(k, dim3(ctas), dim3(C::W * 32), C::kSmem, st, a));
   if (r != SFI_OK || !a.merge_later) return r;
   return cuda_status(launch_k(page_merge_kernel<D, LIST>, dim3(a.B * a.Hq), dim3(kMergeThreads), merge_smem(ctas), st, a));
