@@ -974,7 +974,7 @@ __global__ void __launch_bounds__(kMergeThreads) page_merge_kernel(const __grid_
   const int P = c1 - c0 + 1;
   float4* acc = reinterpret_cast<float4*>(merge_sm);               // [groups][D / 4]
   float2* ml = reinterpret_cast<float2*>(acc + kMergeThreads);     // [P] (m, l)
-  __shared__ float2 warp_ml[kMergeThreads / 32];
+  __shared__ float warp_max[kMergeThreads / 32];
   // only the first piece begins inside its CTA's run
   auto at = [&](int c) { return ((size_t)(c0 + c) * 2 + (c > 0 ? 0 : 1)) * a.G + n; };
   float M = kNoMax;
@@ -984,9 +984,9 @@ __global__ void __launch_bounds__(kMergeThreads) page_merge_kernel(const __grid_
   }
 #pragma unroll
   for (int sh = 16; sh >= 1; sh >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, sh));
-  if (lane == 0) warp_ml[warp].x = M;
+  if (lane == 0) warp_max[warp] = M;
   __syncthreads();
-  for (int w = 0; w < kMergeThreads / 32; ++w) M = fmaxf(M, warp_ml[w].x);
+  for (int w = 0; w < kMergeThreads / 32; ++w) M = fmaxf(M, warp_max[w]);
   constexpr int kSlots = D / 4, kGroups = kMergeThreads / kSlots;
   const int grp = tid / kSlots, slot = tid % kSlots;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
