@@ -774,6 +774,32 @@ def test_rows_in_many_pieces(B, Hq, Hkv, D, lens):
                     check_attn(out[b, hs], lse[b, hs], q[b, hs], K[b, h], V[b, h], (b, h))
 
 
+def test_replay_with_other_lengths_in_many_pieces():
+    """A captured call whose lengths change between replays: rows in many pieces, in one, and empty."""
+    c = Case(3, 32, 2, 64, [4000, 4000, 4000], "e4m3", seed=24).up()
+    S.sfi_quant_store(c.shape, c.kv, c.q8, 0, c.L)
+    V = c.v.float().abs().max().item()
+    lens = torch.full((3,), 4000, dtype=torch.int32, device=DEV)
+    side = torch.cuda.Stream()
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g, stream=side):
+        S.sfi_quant_attn(c.shape, c.q8, c.L, c.qd, c.out, c.ws, lens=lens, lse=c.lse)
+    for now in ([4000, 16, 0], [0, 0, 0], [1600, 4000, 4000], [32, 0, 3984], [4000, 4000, 4000]):
+        lens.copy_(torch.tensor(now, dtype=torch.int32))
+        c.out.fill_(float("nan"))
+        c.lse.fill_(float("nan"))
+        g.replay()
+        assert c.error() == 0
+        out, lse = c.out.cpu().double().numpy(), c.lse.cpu().double().numpy()
+        for b, n in enumerate(now):
+            q = c.q[b].double().numpy()
+            for h in range(2):
+                K, W = c.quant_rows("k", b, h, n), c.quant_rows("v", b, h, n)
+                check_attn(out[b, h * 16:h * 16 + 16], lse[b, h * 16:h * 16 + 16], q[h * 16:h * 16 + 16], K, W, (now, b, h))
+        assert np.abs(out).max() <= 2 * V
+
+
 @pytest.mark.parametrize("Hq", [4, 8, 16])
 def test_nan_stays_where_it_is(Hq):
     """A NaN in one head's query, and a page of values that is not finite."""
