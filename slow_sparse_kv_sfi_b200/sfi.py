@@ -190,8 +190,8 @@ def make_packed(k, v, pos, headmask, n_rows) -> Packed:
 def _arg(t, name, dtypes, shape=None, dev=None):
     """Checks a tensor argument of the 8-bit and block calls (dev: the current device, where known) and
     returns its address."""
-    if (t.dtype in dtypes and (shape is None or t.shape == shape) and t.is_contiguous() and t.is_cuda
-            and t.get_device() == (torch.cuda.current_device() if dev is None else dev)):
+    if (t.dtype in dtypes and (shape is None or t.shape == shape) and t.is_contiguous()
+            and (t.get_device() == dev if dev is not None else t.is_cuda and t.get_device() == torch.cuda.current_device())):
         return t.data_ptr()
     if t.dtype not in dtypes:
         raise ValueError(f"{name}: dtype {t.dtype}, expected {' or '.join(str(d) for d in dtypes)}")
@@ -268,12 +268,15 @@ def _attn_args(shape, q, out, lse, dev):
 
 
 def _sel(shape, sel, dev):
-    if sel.dim() != 3 or sel.shape[0] != shape.B or sel.shape[1] != shape.Hkv:
-        raise ValueError(f"sel: shape {tuple(sel.shape)}, expected ({shape.B}, {shape.Hkv}, at least K)")
-    return _arg(sel, "sel", _I32, None, dev)
+    size = sel.shape
+    if len(size) != 3 or size[0] != shape.B or size[1] != shape.Hkv:
+        raise ValueError(f"sel: shape {tuple(size)}, expected ({shape.B}, {shape.Hkv}, at least K)")
+    return _arg(sel, "sel", _I32, None, dev), size[2]
 
 
 def _ws(ws, dev):
+    if ws.get_device() == dev and ws.is_contiguous():
+        return ws.data_ptr(), ws.nbytes
     return _arg(ws, "ws", (ws.dtype,), None, dev), ws.nbytes
 
 
@@ -464,7 +467,7 @@ def sfi_block_select(shape, index, L, q, n_sink, n_recent, K, sel, ws, lens=None
     _dims(shape, index)
     _check(lib().sfi_block_select(C.byref(shape), C.byref(index), L, _lens(shape.B, lens, dev),
                                   _arg(q, "q", _BF16, (shape.B, shape.Hq, shape.D), dev), n_sink, n_recent, K,
-                                  _sel(shape, sel, dev), sel.shape[-1], *_ws(ws, dev), _on(stream, dev)),
+                                  *_sel(shape, sel, dev), *_ws(ws, dev), _on(stream, dev)),
            "sfi_block_select")
 
 
@@ -472,8 +475,9 @@ def sfi_block_attn(shape, kv, L, q, sel, K, out, ws, lens=None, lse=None, stream
     """Attention over blocks sel[:, :, :K] of the bf16 cache."""
     dev = torch.cuda.current_device()
     q, out, lse = _attn_args(shape, q, out, lse, dev)
-    _check(lib().sfi_block_attn(C.byref(shape), C.byref(kv), L, _lens(shape.B, lens, dev), q, _sel(shape, sel, dev),
-                                sel.shape[-1], K, out, lse, *_ws(ws, dev), _on(stream, dev)), "sfi_block_attn")
+    _check(lib().sfi_block_attn(C.byref(shape), C.byref(kv), L, _lens(shape.B, lens, dev), q,
+                                *_sel(shape, sel, dev), K, out, lse, *_ws(ws, dev), _on(stream, dev)),
+           "sfi_block_attn")
 
 
 def sfi_quant_block_attn(shape, qkv, L, q, sel, K, out, ws, lens=None, lse=None, stream=None):
@@ -482,7 +486,7 @@ def sfi_quant_block_attn(shape, qkv, L, q, sel, K, out, ws, lens=None, lse=None,
     _dims(shape, qkv)
     q, out, lse = _attn_args(shape, q, out, lse, dev)
     _check(lib().sfi_quant_block_attn(C.byref(shape), C.byref(qkv), L, _lens(shape.B, lens, dev), q,
-                                      _sel(shape, sel, dev), sel.shape[-1], K, out, lse, *_ws(ws, dev),
+                                      *_sel(shape, sel, dev), K, out, lse, *_ws(ws, dev),
                                       _on(stream, dev)), "sfi_quant_block_attn")
 
 
