@@ -473,9 +473,10 @@ sfi_status sfi_block_workspace_size(const sfi_shape* shape, size_t* bytes);
  *         sum_d max(q^_hd * hi_jd, q^_hd * lo_jd)
  * with q^ = round(q / e_h), e_h the smallest power of two >= 2^-126 with
  * max |q_h| <= 127 e_h (NaN counts as 0, an infinity as the largest finite
- * value): integers times powers of two, so u is exact in fp32 (clamped to the
- * finite range) and the selection a function of the inputs alone.  Ties go to
- * the lower block.  Blocks that hold one of the first n_sink or the last
+ * value): integers below 2^21 times powers of two, so u is exact in fp32 from
+ * 2^-126 on, rounded once below (ties to even, -0 counts as 0) and clamped to
+ * the finite range, and the selection is a function of the inputs alone.  Ties
+ * go to the lower block.  Blocks that hold one of the first n_sink or the last
  * n_recent tokens are always taken; only the bounds of other blocks, which are
  * full, are read.  K must be at most ceil(L / 16) and at least the smaller of
  * that and ceil(n_sink / 16) + ceil(n_recent / 16) + 1, n_recent >= 1

@@ -6,9 +6,14 @@
 // Since hi >= lo, the maximum is q^+ . hi + q^- . lo with q^+ = max(q^, 0) and
 // q^- = min(q^, 0): one int8 dot product of length 2 D with the page's bounds
 // row [hi | lo], for all heads of the group at once on the int8 tensor path
-// (m16n8k32: 16 pages x 8 heads).  |sum| <= 127 * 127 * D < 2^24 and the
-// scales are powers of two, so u is exact in fp32 and does not depend on the
-// order of the sum.
+// (m16n8k32: 16 pages x 8 heads).  |sum| <= 127 * 127 * D < 2^21 and the
+// scales are powers of two, so u does not depend on the order of the sum: it is
+// rounded once, if it lies below 2^-126, and clamped once, if it is too large.
+// The two scales must not meet the sum one after the other in fp32 as they are:
+// with e_h up to 2^122 and scale_j down to 2^-126 the first product alone can
+// leave the range.  So e_h comes in times 2^-16 (the product then lies between
+// 2^-142, a multiple of the smallest subnormal, and 2^127, and is exact), and
+// the 2^16 goes back in with scale_j (finish_score).
 //
 // Bound by reading 2 D bytes per (page, KV head).  A thread loads the bytes of
 // its fragment straight from global memory: the order of d inside the dot
@@ -58,8 +63,21 @@ __device__ __forceinline__ float tame(float x) {
   return x != x ? 0.f : fminf(fmaxf(x, -big), big);
 }
 
+constexpr float kScoreUnit = 1.f / 65536.f;
+
+// The score from x = 2^-16 max_h sum * e_h and the page's scale: below 1 the
+// scale takes the 2^16 (the product is then rounded once), from 1 on the result
+// does (only a score that is too large overflows on the way).  Clamped to the
+// finite range; -0 becomes +0, its equal.
+__device__ __forceinline__ float finish_score(float x, float scale) {
+  const float big = __uint_as_float(0x7f7fffffu), unit = 1.f / kScoreUnit;
+  const bool small = scale < 1.f;
+  const float u = (x * (small ? scale * unit : scale)) * (small ? 1.f : unit);
+  return __fadd_rn(fminf(fmaxf(u, -big), big), 0.f);
+}
+
 // The group's query codes, as the B operands of the products ([column tile]
-// [16-byte chunk of a thread][lane]), and every head's scale.
+// [16-byte chunk of a thread][lane]), and every head's scale times 2^-16.
 template <int D, int NT>
 struct Query {
   uint4 b[NT][2 * D / 64][32];
@@ -94,7 +112,7 @@ __device__ __forceinline__ void load_query(const SelectArgs& a, int b, int h, Qu
         reinterpret_cast<int8_t*>(&s.b[n / 8][j][(n % 8) * 4 + t])[at % 16] = (int8_t)(half ? min(c, 0) : max(c, 0));
       }
     }
-    if (lane == 0) s.e[n] = __uint_as_float((uint32_t)(ex + 127) << 23);
+    if (lane == 0) s.e[n] = __uint_as_float((uint32_t)(ex + 127) << 23) * kScoreUnit;   // down to 2^-142, exact
   }
   __syncthreads();
 }
@@ -172,15 +190,14 @@ __device__ __forceinline__ void score_tiles(const SelectArgs& a, int h, const Wh
         if (n < a.G) best[j >> 1] = fmaxf(best[j >> 1], (float)d[j] * s.e[n]);
       }
     }
-    const float big = __uint_as_float(0x7f7fffffu);
-    float v[2];
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       best[r] = fmaxf(best[r], __shfl_xor_sync(0xffffffffu, best[r], 1));
       best[r] = fmaxf(best[r], __shfl_xor_sync(0xffffffffu, best[r], 2));
-      v[r] = w[i].page[r] >= 0 ? fminf(fmaxf(best[r] * sc[i][r], -big), big) : w[i].fixed[r];
     }
-    u[i] = t == 0 ? v[0] : v[1];
+    const int r = t & 1;   // the lane's own block: selected before the scale comes in
+    const float v = finish_score(r ? best[1] : best[0], r ? sc[i][1] : sc[i][0]);
+    u[i] = (r ? w[i].page[1] : w[i].page[0]) >= 0 ? v : r ? w[i].fixed[1] : w[i].fixed[0];
   }
 }
 
