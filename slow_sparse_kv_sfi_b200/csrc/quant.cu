@@ -210,6 +210,17 @@ __device__ __forceinline__ void write_bounds(const uint4 (&x)[Lay<D>::NI], const
   const int e = unit_exponent(amax);
   const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
   if (lane == 0) *scale = __uint_as_float((uint32_t)(e + 127) << 23);
+  if (e > 16) {
+    // the quotient of a value far below the scale can underflow to 0 (the
+    // smallest bf16 value is 2^-133, the smallest fp32 one 2^-149), which ceil
+    // and floor would keep; any value up to the scale gives the same bound
+    const float least = __uint_as_float((uint32_t)(e + 127 - 20) << 23);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      if (hi[k] > 0.f) hi[k] = fmaxf(hi[k], least);
+      if (lo[k] < 0.f) lo[k] = fminf(lo[k], -least);
+    }
+  }
   if (lane < Y::CH) {
     uint32_t ph[2] = {0u, 0u}, pl[2] = {0u, 0u};
 #pragma unroll

@@ -62,3 +62,31 @@ def test_select_scores_at_the_ends_of_the_range(what, D, Hq):
     else:
         assert np.abs(u).max() < big and len(set(u)) > 30
     assert np.array_equal(sel[0, 0].cpu().numpy(), P.select(u, n, 0, 1, K))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("top", [math.inf, P.BF16_MAX, 1.0])
+def test_bounds_of_dimensions_far_apart(D, top):
+    """A dimension whose values are far below the page's unit still gets outward bounds: 1 above
+    zero, -1 below it."""
+    c = Case(1, 2, 2, D, [32], seed=32)
+    tiny = (1e-12, -1e-12, 1e-39, -1e-39, 0.0)
+    for j in range(2):
+        page = c.k[int(c.pt[0, j])]
+        page[:, :, :5] = torch.tensor(tiny)
+        page[:, 3, 7] = top * (1 - 2 * j)
+    c.up()
+    S.sfi_quant_store(c.shape, c.kv, c.q8, 0, 32, index=c.ix)
+    got = [(c.bounds.clone(), c.bscale.clone())]
+    c.bounds.fill_(77)
+    S.sfi_block_build(c.shape, c.kv, c.ix, 0, 32)
+    got.append((c.bounds.clone(), c.bscale.clone()))
+    assert c.error() == 0
+    for bounds, scale in got:
+        for j in range(2):
+            p = int(c.pt[0, j])
+            for h in range(2):
+                codes, u = P.page_bounds(c.k[p, h].double().numpy())
+                assert codes[0, 0] == 1 and codes[1, 1] == -1 and codes[0, 2] == 1 and codes[1, 3] == -1
+                assert np.array_equal(bounds[p, h].cpu().numpy().astype(np.int64), codes), (j, h)
+                assert float(scale[p, h]) == u
