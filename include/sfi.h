@@ -440,7 +440,8 @@ sfi_status sfi_quant_load(const sfi_shape* shape, const sfi_quant_kv* qkv, const
  *  out  fp32 [B, Hq, D] = sum_j softmax(z)_j v_j, z_j = q.k_j / sqrt(D)
  *  lse  fp32 [B, Hq] natural-log sum of exp(z), or NULL
  *       (out 16-byte aligned)
- * An empty sequence gets out = 0 and lse = -infinity.  ws: scratch of
+ * The output is a mean of the values: finite values of any size give a finite
+ * one.  An empty sequence gets out = 0 and lse = -infinity.  ws: scratch of
  * sfi_block_workspace_size bytes, 16-byte aligned, zero-filled before its first
  * use; every call leaves it ready for the next one that takes it, of any shape
  * whose size it has.  Calls that share one ws must not run concurrently. */

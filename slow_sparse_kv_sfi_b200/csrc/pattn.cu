@@ -51,9 +51,12 @@ namespace sfi {
 namespace {
 
 constexpr int kBf16 = 2;            // FMT: SFI_FMT_E4M3, SFI_FMT_INT8 or this
-// A warp's reference m is set kBias below its largest logit so far (log2 units)
-// and moves when a logit exceeds it by kBias + kSlack: P reaches 2^14, inside
-// fp16, and is held to 2^-24 * 2^-8 of the largest one below that.
+// A warp's reference m is set `bias` below its largest logit so far (log2 units)
+// and moves when a logit exceeds it by bias + kSlack.  8-bit pages, kBias: P
+// reaches 2^14, inside fp16, and is held to 2^-24 * 2^-8 of the largest one below
+// that.  bf16 pages: O = sum P v is as large as l times the largest |v|, which
+// may be the type's largest, so the reference lies above the logits, by enough
+// that l <= 1/2 over all tokens of a row (bf16 holds any P alike).
 constexpr float kBias = 8.f, kSlack = 6.f;
 constexpr float kNoMax = -3.4028234663852886e38f;   // m before the first logit
 
@@ -78,9 +81,11 @@ struct PageAttnArgs {
   int merge_later;                  // pieces are merged by the next kernel
   int pieces;                       // > 0: CTAs of each row, whose runs begin with the row; 0: even runs
   float scale_log2;                 // log2(e) / sqrt(D)
+  float bias;                       // of the reference m below the largest logit (kBias: 8-bit pages)
+  float tail_unit;                  // unit of the tail's share of O: P |v| / tail_unit stays finite (8-bit pages)
   float* out;
   float* lse;
-  float* part;                      // [cta][2][G][D]: piece of the row that began before, that goes on behind
+  float* part;                      // [cta][2][G][D] mean of values: piece of the row that began before, that goes on behind
   float* ml;                        // [cta][2][G][2]
   int* arrived;                     // [B * Hkv] pieces of a row written so far; zero between calls
   int* err;
@@ -305,11 +310,13 @@ __device__ __forceinline__ void scale_o(State<D, NT>& st, float f) {
 // One tile from its fragments: kf(step, a) and vf(step, a) fill the A operands
 // of S^T and O^T, qf(column tile, step, b0, b1) the B operand of S^T; between()
 // runs once K is used up.  zf: log2 units per unit of S^T, per head; vs: the
-// value scale; rows: valid rows.  F16: fp16 operands (8-bit pages), else bf16.
-// SCALED: the cache has value scales.
-template <int D, int HM, bool F16, bool SCALED, class KF, class QF, class BW, class VF, int NT>
-__device__ __forceinline__ void tile_math(State<D, NT>& st, const float (&zf)[NT][2], float vs, int rows, int lane,
-                                          KF kf, QF qf, BW between, VF vf) {
+// value scale, or the tail's unit; bias: of the reference; rows: valid rows.  F16: fp16 operands (8-bit pages), else bf16.
+// SCALED: the cache has value scales.  UNROLL: of the rescaling of O, 1 or 2; rolled
+// it costs the list kernel of 16 heads fewer registers (64K, 820 blocks, 64/4 heads:
+// 93.5 -> 90.1 us), the one without a list runs better unrolled (64K 251.9, 245.4).
+template <int D, int HM, bool F16, bool SCALED, int UNROLL, class KF, class QF, class BW, class VF, int NT>
+__device__ __forceinline__ void tile_math(State<D, NT>& st, const float (&zf)[NT][2], float vs, float bias, int rows,
+                                          int lane, KF kf, QF qf, BW between, VF vf) {
   float s[NT][4], x[NT][4];
 #pragma unroll
   for (int k = 0; k < D / 16; ++k) {
@@ -334,7 +341,7 @@ __device__ __forceinline__ void tile_math(State<D, NT>& st, const float (&zf)[NT
       s[nt][i] += x[nt][i];
       x[nt][i] = fmaf(s[nt][i], zf[nt][i & 1], -st.m[nt][i & 1]);   // one rounding, of the difference
       if (!F16 && rows < kPage && (lane >> 2) + 8 * (i >> 1) >= rows) x[nt][i] = -INFINITY;   // 8-bit pages are full
-      grow |= x[nt][i] > kBias + kSlack;
+      grow |= x[nt][i] > bias + kSlack;
     }
   if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
@@ -347,7 +354,7 @@ __device__ __forceinline__ void tile_math(State<D, NT>& st, const float (&zf)[NT
           if (x[nt][j + 2 * r] != -INFINITY) z = fmaxf(z, s[nt][j + 2 * r] * zf[nt][j]);
 #pragma unroll
         for (int sh = 4; sh <= 16; sh <<= 1) z = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, sh));
-        const float mn = fmaxf(st.m[nt][j], z - kBias);
+        const float mn = fmaxf(st.m[nt][j], z - bias);
         const float al = fast_exp2(st.m[nt][j] - mn);
         st.m[nt][j] = mn;
         st.l[nt][j] *= al;
@@ -369,11 +376,15 @@ __device__ __forceinline__ void tile_math(State<D, NT>& st, const float (&zf)[NT
   bool apart = false;
   if constexpr (SCALED) {
     if (!(vs <= 2.f * st.vref)) {   // NaN too
-      scale_o(st, __fdiv_rn(st.vref, vs));
-      st.vref = vs;
+      // O times vref / vs: in two steps, since the quotient alone may leave fp32's
+      // range, the first being the one that keeps the product inside it
       st.vinv = __fdiv_rn(1.f, vs);
+      const bool large = vs >= 1.f;
+#pragma unroll UNROLL
+      for (int i = 0; i < 2; ++i) scale_o(st, (i == 0) == large ? st.vinv : st.vref);
+      st.vref = vs;
     }
-    pv = vs * st.vinv;
+    pv = F16 ? vs * st.vinv : st.vinv;   // the tail's values have no scale
     // the same in every lane; the vote lets the compiler branch
     if (F16) apart = __any_sync(0xffffffffu, pv < 0.015625f);
   }
@@ -411,7 +422,7 @@ __device__ __forceinline__ void tile_math(State<D, NT>& st, const float (&zf)[NT
         mma16<F16, false>(c, a, hi[nt][0], hi[nt][1]);
         if constexpr (HM != kHalf) mma16<F16, true>(c, a, lo[nt][0], lo[nt][1]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) st.o[nt][k][i] = fmaf(pv, c[i], st.o[nt][k][i]);
+        for (int i = 0; i < 4; ++i) st.o[nt][k][i] = fmaf(c[i] * vs, st.vinv, st.o[nt][k][i]);   // pv may be subnormal
       }
     }
   } else {
@@ -435,14 +446,28 @@ __device__ __forceinline__ void add_scaled(float4& o, float f, const float4& x) 
   o.w = fmaf(f, x.w, o.w);
 }
 
-// Columns d .. d + 3 of an output row (and its log-sum-exp) from (m, l, O);
-// l = 0: nothing to attend to.
+// 1 / sum of the weights of a merge, off by at most 2^-23 of itself (sums lie
+// between 2^-50 and 2^50; a division in fp32's full range took 0.5 us of a short
+// call); nothing to attend to: 0.
+__device__ __forceinline__ float inverse(float l) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(l));
+  return l == 0.f ? 0.f : r;
+}
+
+// Columns d .. d + 3 of an output row, the mean o of the values, and its
+// log-sum-exp from (m, l); l = 0: nothing to attend to.  l's exponent joins m
+// first, so that the logarithm's error is not one of a large l's.
 template <int D>
 __device__ __forceinline__ void write_out(const PageAttnArgs& a, size_t row, int d, float M, float l, const float4& o) {
   const bool none = l == 0.f;
-  const float r = none ? 0.f : __fdiv_rn(1.f, l);
-  *reinterpret_cast<float4*>(a.out + row * D + d) = make_float4(o.x * r, o.y * r, o.z * r, o.w * r);
-  if (d == 0 && a.lse) a.lse[row] = none ? -INFINITY : (M + fast_log2(l)) * kLn2;
+  *reinterpret_cast<float4*>(a.out + row * D + d) = none ? make_float4(0.f, 0.f, 0.f, 0.f) : o;
+  if (d == 0 && a.lse) {
+    const uint32_t u = __float_as_uint(l);
+    const float e = (float)((int)(u >> 23) - 127);
+    const float lse = ((M + e) + fast_log2(__uint_as_float((u & 0x7fffffu) | 0x3f800000u))) * kLn2;
+    a.lse[row] = none ? -INFINITY : l != l ? l : lse;
+  }
 }
 
 constexpr int kMaxGroups = 8;
@@ -466,6 +491,7 @@ __device__ __forceinline__ void attend_row(const PageAttnArgs& a, uint8_t* smem,
                                            int t1, int c0, int c1) {
   using C = Cfg<D, FMT, HM>;
   constexpr int NT = C::NT, W = C::W, KJ = C::KJ, VC = C::VC;
+  constexpr int kUnroll = LIST && HM == kTwo ? 1 : 2;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const int bh = b * a.Hkv + h;
@@ -668,8 +694,8 @@ __device__ __forceinline__ void attend_row(const PageAttnArgs& a, uint8_t* smem,
     };
     if (cur.page >= 0) {
       if constexpr (FMT == kBf16) {
-        tile_math<D, HM, false, false>(
-            st, zq, 1.f, cur.rows, lane,
+        tile_math<D, HM, false, false, 2>(
+            st, zq, 1.f, a.bias, cur.rows, lane,
             [&](int k, uint32_t (&f)[4]) {
               const int w = (k % 2) * 2;
               f[0] = word(kx[k / 2], w);
@@ -693,8 +719,8 @@ __device__ __forceinline__ void attend_row(const PageAttnArgs& a, uint8_t* smem,
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int j = 0; j < 2; ++j) zf[nt][j] = zq[nt][j] * cur.ks;
-        tile_math<D, HM, true, true>(
-            st, zf, cur.vs, kPage, lane,
+        tile_math<D, HM, true, true, kUnroll>(
+            st, zf, cur.vs, kBias, kPage, lane,
             [&](int k, uint32_t (&f)[4]) {
               to_f16<FMT>(word(kx[k / 4], k % 4), f[0], f[2]);
               to_f16<FMT>(word(kx[KJ + k / 4], k % 4), f[1], f[3]);
@@ -720,8 +746,8 @@ __device__ __forceinline__ void attend_row(const PageAttnArgs& a, uint8_t* smem,
       float zt[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) zt[nt][0] = zt[nt][1] = a.scale_log2;
-        tile_math<D, HM, false, true>(
-            st, zt, 1.f, tail_rows, lane,
+        tile_math<D, HM, false, true, kUnroll>(
+            st, zt, a.tail_unit, kBias, tail_rows, lane,
             [&](int k, uint32_t (&f)[4]) {
               const int d = C::k_col(t, k);
               uint2 x = make_uint2(0, 0), y = make_uint2(0, 0);
@@ -756,8 +782,10 @@ __device__ __forceinline__ void attend_row(const PageAttnArgs& a, uint8_t* smem,
     cur = nxt;
   }
 
-  // Merge of the CTA's warps: O of each head, row of D floats padded by 8,
-  // then (m, l) of each head.
+  // Merge of the CTA's warps: O / l of each head, row of D floats padded by 8,
+  // then (m, l) of each head.  From here on everything is a mean of values with
+  // weights that add up to 1: it stays finite when the values are the type's
+  // largest, where O and l apart would not.
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -770,12 +798,12 @@ __device__ __forceinline__ void attend_row(const PageAttnArgs& a, uint8_t* smem,
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int k = 0; k < D / 16; ++k) {
-      const int d = C::v_col(g, k);
+    for (int j = 0; j < 2; ++j) {
+      const float r = inverse(st.l[nt][j]);
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
-        *reinterpret_cast<float2*>(so + (size_t)(warp * NT * 8 + nt * 8 + 2 * t + j) * kLd + d) =
-            make_float2(st.o[nt][k][j] * st.vref, st.o[nt][k][j + 2] * st.vref);
+      for (int k = 0; k < D / 16; ++k)
+        *reinterpret_cast<float2*>(so + (size_t)(warp * NT * 8 + nt * 8 + 2 * t + j) * kLd + C::v_col(g, k)) =
+            make_float2(st.o[nt][k][j] * r * st.vref, st.o[nt][k][j + 2] * r * st.vref);
     }
   if (g == 0) {
 #pragma unroll
@@ -793,13 +821,18 @@ __device__ __forceinline__ void attend_row(const PageAttnArgs& a, uint8_t* smem,
     float M = kNoMax;
 #pragma unroll
     for (int w = 0; w < W; ++w) M = fmaxf(M, sml[(w * NT * 8 + n_) * 2]);
-    float l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = 0.f, weight[W];
 #pragma unroll
     for (int w = 0; w < W; ++w) {
       const float2 ml = *reinterpret_cast<const float2*>(sml + (w * NT * 8 + n_) * 2);
-      const float f = fast_exp2(ml.x - M);
-      l += f * ml.y;
+      weight[w] = fast_exp2(ml.x - M) * ml.y;
+      l += weight[w];
+    }
+    const float r = inverse(l);
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const float f = weight[w] * r;
       add_scaled(o, f, *reinterpret_cast<const float4*>(so + (w * NT * 8 + n_) * kLd + d));
       if (HM == kHalf) add_scaled(o, f, *reinterpret_cast<const float4*>(so + (w * 8 + n_ + 4) * kLd + d));
     }
@@ -846,15 +879,18 @@ __device__ __forceinline__ void attend_row(const PageAttnArgs& a, uint8_t* smem,
         x[i] = ci <= c1 ? __ldcg(reinterpret_cast<const float4*>(a.part + r * D + d)) : make_float4(0.f, 0.f, 0.f, 0.f);
       }
       const float mn = fmaxf(fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), M);
-      const float f = fast_exp2(M - mn);
-      l *= f;
-      o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+      float f = l * fast_exp2(M - mn), sum = f;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float fi = fast_exp2(ml[i].x - mn);
-        l += ml[i].y * fi;
-        add_scaled(o, fi, x[i]);
+        ml[i].y *= fast_exp2(ml[i].x - mn);
+        sum += ml[i].y;
       }
+      const float r = inverse(sum);
+      f *= r;
+      o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) add_scaled(o, ml[i].y * r, x[i]);
+      l = sum;
       M = mn;
     }
     if (groups == 1) {
@@ -873,9 +909,12 @@ __device__ __forceinline__ void attend_row(const PageAttnArgs& a, uint8_t* smem,
     for (int i = 0; i < groups; ++i) M = fmaxf(M, so[(i * slots + slot) * 8 + 4]);
     for (int i = 0; i < groups; ++i) {
       const float* g_ = so + (i * slots + slot) * 8;
-      const float f = fast_exp2(g_[4] - M);
-      l += f * g_[5];
-      add_scaled(o, f, *reinterpret_cast<const float4*>(g_));
+      l += fast_exp2(g_[4] - M) * g_[5];
+    }
+    const float r = inverse(l);
+    for (int i = 0; i < groups; ++i) {
+      const float* g_ = so + (i * slots + slot) * 8;
+      add_scaled(o, fast_exp2(g_[4] - M) * g_[5] * r, *reinterpret_cast<const float4*>(g_));
     }
     write_out<D>(a, (size_t)b * a.Hq + h * a.G + slot / (D / 4), slot % (D / 4) * 4, M, l, o);
   }
@@ -974,27 +1013,37 @@ __global__ void __launch_bounds__(kMergeThreads) page_merge_kernel(const __grid_
   const int P = c1 - c0 + 1;
   float4* acc = reinterpret_cast<float4*>(merge_sm);               // [groups][D / 4]
   float2* ml = reinterpret_cast<float2*>(acc + kMergeThreads);     // [P] (m, l)
-  __shared__ float warp_max[kMergeThreads / 32];
+  __shared__ float2 warp_max[kMergeThreads / 32];
   // only the first piece begins inside its CTA's run
   auto at = [&](int c) { return ((size_t)(c0 + c) * 2 + (c > 0 ? 0 : 1)) * a.G + n; };
-  float M = kNoMax;
+  float M = kNoMax, top = 0.f;   // the largest m and l
   for (int c = tid; c < P; c += kMergeThreads) {
     ml[c] = __ldcg(reinterpret_cast<const float2*>(a.ml + at(c) * 2));
     M = fmaxf(M, ml[c].x);
+    top = fmaxf(top, ml[c].y);
   }
 #pragma unroll
-  for (int sh = 16; sh >= 1; sh >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, sh));
-  if (lane == 0) warp_max[warp] = M;
+  for (int sh = 16; sh >= 1; sh >>= 1) {
+    M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, sh));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, sh));
+  }
+  if (lane == 0) warp_max[warp] = make_float2(M, top);
   __syncthreads();
-  for (int w = 0; w < kMergeThreads / 32; ++w) M = fmaxf(M, warp_max[w]);
+  for (int w = 0; w < kMergeThreads / 32; ++w) {
+    M = fmaxf(M, warp_max[w].x);
+    top = fmaxf(top, warp_max[w].y);
+  }
+  // weights times 2^-k, which keeps their sum at or below 1
+  const int k = (int)(__float_as_uint(top) >> 23) - 126 + (32 - __clz(P));
+  const float unit = __uint_as_float((uint32_t)(127 - k) << 23);
   constexpr int kSlots = D / 4, kGroups = kMergeThreads / kSlots;
   const int grp = tid / kSlots, slot = tid % kSlots;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   float l = 0.f;   // of this group's pieces
 #pragma unroll 8
   for (int c = grp; c < P; c += kGroups) {
-    const float f = fast_exp2(ml[c].x - M);
-    l += f * ml[c].y;
+    const float f = fast_exp2(ml[c].x - M) * (ml[c].y * unit);
+    l += f;
     add_scaled(o, f, __ldcg(reinterpret_cast<const float4*>(a.part + at(c) * D + slot * 4)));
   }
   acc[tid] = o;
@@ -1005,6 +1054,9 @@ __global__ void __launch_bounds__(kMergeThreads) page_merge_kernel(const __grid_
   for (int i = 1; i < kGroups; ++i) add_scaled(o, 1.f, acc[i * kSlots + slot]);
   l = 0.f;
   for (int i = 0; i < kGroups; ++i) l += group_l[i];
+  const float r = inverse(l);
+  o = make_float4(o.x * r, o.y * r, o.z * r, o.w * r);
+  l *= __uint_as_float((uint32_t)(127 + k) << 23);
   write_out<D>(a, (size_t)b * a.Hq + hq, slot * 4, M, l, o);
 }
 
@@ -1131,6 +1183,13 @@ sfi_status run(const sfi_shape* shape, const sfi_paged_kv* kv, const sfi_quant_k
   a.sel_ld = sel_ld;
   a.K = K;
   a.scale_log2 = kLog2e / sqrtf((float)shape->D);
+  // bits that the tokens a warp can meet take: P up to 2^(bias + kSlack) each
+  // stay below 1/2 in all (bf16 pages); tails listed K times, P up to 2^14 for 16
+  // tokens each, stay 2^2 below fp32's range (8-bit pages)
+  int bits = 0;
+  while ((1ll << bits) < (list ? K : 1)) ++bits;
+  a.bias = q8 ? kBias : -(float)(bits + 4 + 1) - kSlack;
+  a.tail_unit = ldexpf(1.f, 20 + bits);
   a.out = out;
   a.lse = lse;
   a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + w.part_off);

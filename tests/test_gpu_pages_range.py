@@ -90,3 +90,90 @@ def test_bounds_of_dimensions_far_apart(D, top):
                 assert codes[0, 0] == 1 and codes[1, 1] == -1 and codes[0, 2] == 1 and codes[1, 3] == -1
                 assert np.array_equal(bounds[p, h].cpu().numpy().astype(np.int64), codes), (j, h)
                 assert float(scale[p, h]) == u
+
+
+# ------------------------------------------------------------------ attention
+@pytest.mark.parametrize("B,Hq,Hkv,D,lens", [
+    (1, 3, 1, 64, [1]), (4, 6, 1, 128, [5, 16, 0, 17]), (1, 13, 1, 128, [300]), (2, 8, 2, 128, [5000, 31]),
+    (1, 16, 1, 64, [9001])])
+@pytest.mark.parametrize("equal", [False, True])
+def test_values_near_the_largest(B, Hq, Hkv, D, lens, equal):
+    """Values up to the largest bf16 one, in full pages and in the page that is not full, logits that rise
+    along the sequence: the weighted mean is finite, and the output is it."""
+    c = Case(B, Hq, Hkv, D, lens, seed=33, slack=1)
+    size = torch.ones_like(c.v, dtype=torch.float64) if equal else torch.rand(c.v.shape, generator=c.g, dtype=torch.float64) * 0.5 + 0.5
+    sign = 1.0 if equal else torch.where(torch.rand(c.v.shape, generator=c.g) < 0.3, -1.0, 1.0)
+    c.v = (size * P.BF16_MAX * sign).to(torch.bfloat16)
+    assert torch.isfinite(c.v).all()
+    nb = -(-c.L // PAGE)
+    for j in range(nb):
+        for b in range(B):
+            p = int(c.pt[b, j])
+            c.k[p] = (c.k[p].float() * (0.3 + j / nb)).to(torch.bfloat16)
+    sel = torch.arange(nb, dtype=torch.int32).flip(0).expand(B, Hkv, nb).contiguous().to(DEV)
+    for fmt in FMTS:
+        c.fmt = fmt
+        c.up()
+        S.sfi_quant_store(c.shape, c.kv, c.q8, 0, c.L, lens=c.lend)
+        K, V = {}, {}
+        for b, n in enumerate(lens):
+            for h in range(Hkv):
+                K[b, h], V[b, h] = c.quant_rows("k", b, h, n), c.quant_rows("v", b, h, n)
+        for call in (lambda: S.sfi_quant_attn(c.shape, c.q8, c.L, c.qd, c.out, c.ws, lens=c.lend, lse=c.lse),
+                     lambda: S.sfi_quant_block_attn(c.shape, c.q8, c.L, c.qd, sel, nb, c.out, c.ws, lens=c.lend, lse=c.lse)):
+            c.out.fill_(float("nan"))
+            call()
+            assert c.error() == 0
+            assert torch.isfinite(c.out).all()
+            check_all(c, lambda b, h, n: K[b, h], lambda b, h, n: V[b, h])
+    c.out.fill_(float("nan"))
+    S.sfi_block_attn(c.shape, c.kv, c.L, c.qd, sel, nb, c.out, c.ws, lens=c.lend, lse=c.lse)
+    assert c.error() == 0
+    assert torch.isfinite(c.out).all()
+    check_all(c, lambda b, h, n: c.rows(c.k, b, h, n), lambda b, h, n: c.rows(c.v, b, h, n))
+
+
+@pytest.mark.parametrize("Hq", [4, 16])
+def test_one_block_of_the_largest_values_many_times(Hq):
+    """The page that is not full, with values of the largest size, listed 500 times; and a full one."""
+    K, n = 500, 40
+    for block in (1, 2):
+        c = Case(1, Hq, 1, 64, [n], "e4m3", seed=34, slack=K)
+        c.v[:] = P.BF16_MAX
+        c.up()
+        sel = torch.full((1, 1, K), block, dtype=torch.int32, device=DEV)
+        S.sfi_quant_store(c.shape, c.kv, c.q8, 0, n)
+        kq, vq = c.quant_rows("k", 0, 0, n, [block]), c.quant_rows("v", 0, 0, n, [block])
+        S.sfi_quant_block_attn(c.shape, c.q8, n, c.qd, sel, K, c.out, c.ws, lse=c.lse)
+        assert c.error() == 0
+        check_all(c, lambda b, h, m: np.concatenate([kq] * K), lambda b, h, m: np.concatenate([vq] * K))
+        S.sfi_block_attn(c.shape, c.kv, n, c.qd, sel, K, c.out, c.ws, lse=c.lse)
+        assert c.error() == 0
+        check_all(c, lambda b, h, m: listed(c, c.k, b, h, m, [block] * K), lambda b, h, m: listed(c, c.v, b, h, m, [block] * K))
+
+
+@pytest.mark.parametrize("Hq", [4, 8, 16])
+def test_largest_values_without_weight(Hq):
+    """Values of the largest size where the logits are hundreds lower: the others keep their precision,
+    in 8-bit pages, in the page that is not full and in bf16 pages."""
+    n, D = 12 * PAGE + 9, 64
+    c = Case(1, Hq, 1, D, [n], "int8", seed=35)
+    unit = torch.zeros(D)
+    unit[0] = 1.0
+    for j in range(13):
+        p = int(c.pt[0, j])
+        far = j in (1, 6)
+        if far:
+            c.v[p] = P.BF16_MAX
+        c.k[p] = (c.k[p].float() * 0.3 + unit * (-300.0 if far else 0.0)).to(torch.bfloat16)
+    c.q[0, :, 0] = 12.0
+    c.up()
+    S.sfi_quant_store(c.shape, c.kv, c.q8, 0, n)
+    S.sfi_quant_attn(c.shape, c.q8, n, c.qd, c.out, c.ws, lse=c.lse)
+    assert c.error() == 0
+    assert float(c.out.abs().max()) < 10
+    check_all(c, lambda b, h, m: c.quant_rows("k", b, h, m), lambda b, h, m: c.quant_rows("v", b, h, m))
+    sel = torch.arange(13, dtype=torch.int32, device=DEV).view(1, 1, 13)
+    S.sfi_block_attn(c.shape, c.kv, n, c.qd, sel, 13, c.out, c.ws, lse=c.lse)
+    assert c.error() == 0
+    check_all(c, lambda b, h, m: c.rows(c.k, b, h, m), lambda b, h, m: c.rows(c.v, b, h, m))
