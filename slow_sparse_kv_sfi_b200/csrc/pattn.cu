@@ -53,8 +53,12 @@ namespace {
 constexpr int kBf16 = 2;            // FMT: SFI_FMT_E4M3, SFI_FMT_INT8 or this
 // A warp's reference m is set `bias` below its largest logit so far (log2 units)
 // and moves when a logit exceeds it by bias + kSlack.  8-bit pages, kBias: P
-// reaches 2^14, inside fp16, and is held to 2^-24 * 2^-8 of the largest one below
-// that.  bf16 pages: O = sum P v is as large as l times the largest |v|, which
+// reaches 2^14, inside fp16, and the largest one is at least 2^8.  What fp16 holds
+// is P times pv = scale / vref (tile_math), in two parts, the second in steps of at
+// least 2^-24: a weight is off by at most 2^-25 / pv, 2^-33 / pv of the largest, so
+// 2^-33 on pages of the largest scale and 2^-27 at pv = 2^-6, where the factor is
+// taken out.  The error times the page's values, whose size goes with pv, stays
+// below 2^-33 of the largest page's.  bf16 pages: O = sum P v is as large as l times the largest |v|, which
 // may be the type's largest, so the reference lies above the logits, by enough
 // that l <= 1/2 over all tokens of a row (bf16 holds any P alike).
 constexpr float kBias = 8.f, kSlack = 6.f;
@@ -370,7 +374,7 @@ __device__ __forceinline__ void tile_math(State<D, NT>& st, const float (&zf)[NT
   }
   // The value scale multiplies P, relative to vref so that fp16 holds it: vref
   // follows the largest scale seen (within a factor of 2); a page whose scale
-  // is 2^6 and more below it, which fp16 would hold less exactly, has its
+  // is 2^6 and more below it, which fp16 would hold to fewer than 2^-27, has its
   // product scaled instead.
   float pv = 1.f;
   bool apart = false;

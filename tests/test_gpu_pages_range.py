@@ -177,3 +177,52 @@ def test_largest_values_without_weight(Hq):
     S.sfi_block_attn(c.shape, c.kv, n, c.qd, sel, 13, c.out, c.ws, lse=c.lse)
     assert c.error() == 0
     check_all(c, lambda b, h, m: c.rows(c.k, b, h, m), lambda b, h, m: c.rows(c.v, b, h, m))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("D,Hq", [(64, 4), (128, 7), (128, 16)])
+@pytest.mark.parametrize("low,below", [((22.0, 30.0), [3, 7, 12, 20, 33, 50, 60, 63]), ((27.5, 28.0), [50, 52, 54, 56, 58, 60, 62, 63])])
+def test_weights_of_pages_below_the_largest(fmt, D, Hq, low, below):
+    """Pages whose value scales are 2 to 60 times below the largest, small weights on them, and nearly all the
+    weight on a token whose values are zero.
+
+    P times (scale / largest scale so far) is held as two fp16 parts, the second with steps of at least
+    2^-24: off by at most 2^-25.  The largest P is at least 2^8 and the factor at least 2^-6 (pages below that
+    take their factor behind the product), so a weight p = P / sum P is off by at most 2^-27 on top of what
+    check_attn's other terms allow, or by itself where it is smaller."""
+    below = [1] * 8 + below   # a page of the largest values first in each of up to 8 warps
+    n = len(below) * PAGE
+    c = Case(1, Hq, 1, D, [n], fmt, seed=36)
+    unit = torch.zeros(D)
+    unit[0] = 1.0
+    for j, f in enumerate(below):
+        p = int(c.pt[0, j])
+        x = torch.randn(PAGE, D, generator=c.g)
+        c.v[p, 0] = (x.abs() / x.abs().max() * (64.0 / f)).to(torch.bfloat16)
+        # logits so far (in powers of two) below the largest one's
+        less = low[0] + (low[1] - low[0]) * torch.rand(PAGE, 1, generator=c.g)
+        c.k[p, 0] = (unit * (-less * math.log(2.0) * math.sqrt(D) / 8.0)).to(torch.bfloat16)
+        if j < 8:
+            c.k[p, 0] = (unit * -300.0).to(torch.bfloat16)    # the largest values: no weight at all
+            c.k[p, 0, 0] = 0.0
+            c.v[p, 0, 0] = 0.0
+    c.q[:] = 0.0
+    c.q[0, :, 0] = 8.0
+    c.up()
+    S.sfi_quant_store(c.shape, c.kv, c.q8, 0, n)
+    K, V = c.quant_rows("k", 0, 0, n), c.quant_rows("v", 0, 0, n)
+    nb = len(below)
+    sel = torch.arange(nb, dtype=torch.int32, device=DEV).view(1, 1, nb)
+    for call in (lambda: S.sfi_quant_attn(c.shape, c.q8, n, c.qd, c.out, c.ws),
+                 lambda: S.sfi_quant_block_attn(c.shape, c.q8, n, c.qd, sel, nb, c.out, c.ws)):
+        c.out.fill_(float("nan"))
+        call()
+        assert c.error() == 0
+        q = c.q[0].double().numpy()
+        o, _, pv, s = P.attention(q, K, V)
+        dz = (D / 16 + 2) * 2.0 ** -23 * s + 2.0 ** -22 * s
+        rel = 2.0 ** -16 + 2 * dz + (nb + 64) * 2.0 ** -23
+        z = q @ K.T / math.sqrt(D)
+        p = np.exp(z - z.max(1, keepdims=True))
+        got = c.out[0].cpu().double().numpy()
+        assert np.all(np.abs(got - o) <= rel[:, None] * pv + np.minimum(2.0 ** -27, p) @ np.abs(V) + 1e-30)
