@@ -177,9 +177,18 @@ def make_params(n_sink, n_recent, k_fixed, budget_frac, lam, lam_clip, alpha_sof
 
 
 def make_kv(k_pool, v_pool, page_table, key_norms=None, err=None) -> PagedKV:
-    return PagedKV(k_pool.data_ptr(), v_pool.data_ptr(), page_table.data_ptr(),
-                   None if key_norms is None else key_norms.data_ptr(),
-                   None if err is None else err.data_ptr())
+    kv = PagedKV(k_pool.data_ptr(), v_pool.data_ptr(), page_table.data_ptr(),
+                 None if key_norms is None else key_norms.data_ptr(),
+                 None if err is None else err.data_ptr())
+    # the sizes that the 8-bit and block calls check against their shape: None when the
+    # tensors are not pools of bf16 pages and a table of them, which those calls refuse
+    kv.dims = None
+    if (k_pool.dim() == 4 and k_pool.shape == v_pool.shape and k_pool.shape[2] == 16 and page_table.dim() == 2
+            and k_pool.dtype == v_pool.dtype == torch.bfloat16 and page_table.dtype == torch.int32
+            and k_pool.is_contiguous() and v_pool.is_contiguous() and page_table.is_contiguous()):
+        kv.dims = (page_table.shape[0], k_pool.shape[1], k_pool.shape[3], page_table.shape[1], k_pool.shape[0])
+    kv.device = k_pool.get_device()
+    return kv
 
 
 def make_packed(k, v, pos, headmask, n_rows) -> Packed:
@@ -216,23 +225,27 @@ def _on(stream, dev):
 
 
 _BF16, _F32, _I32 = (torch.bfloat16,), (torch.float32,), (torch.int32,)
-_CODES = (torch.uint8, torch.int8, torch.float8_e4m3fn)
+_CODES = {FMT_E4M3: (torch.uint8, torch.float8_e4m3fn), FMT_INT8: (torch.uint8, torch.int8)}   # by format
 
 
 def make_quant_kv(k_pool, v_pool, k_scale, v_scale, k_tail, v_tail, page_table, fmt, err=None) -> QuantKV:
-    """k_pool, v_pool: 8-bit [num_pages, Hkv, 16, D]; scales: fp32 [num_pages, Hkv]; tails: bf16
-    [B, Hkv, 16, D]; page_table: int32 [B, max_pages]; fmt: FMT_E4M3 or FMT_INT8.  The caller keeps the
-    tensors alive."""
+    """k_pool, v_pool: uint8 or the format's own type [num_pages, Hkv, 16, D]; scales: fp32 [num_pages, Hkv];
+    tails: bf16 [B, Hkv, 16, D]; page_table: int32 [B, max_pages]; fmt: FMT_E4M3 or FMT_INT8.  The caller
+    keeps the tensors alive."""
     n, hkv, rows, d = k_pool.shape
     b, max_pages = page_table.shape
     if rows != 16:
         raise ValueError("k_pool: pages have 16 rows")
+    codes = _CODES.get(fmt)
+    if codes is None:
+        raise ValueError(f"fmt: {fmt}, expected FMT_E4M3 or FMT_INT8")
     tail = (b, hkv, 16, d)
-    kv = QuantKV(_arg(k_pool, "k_pool", _CODES), _arg(v_pool, "v_pool", _CODES, (n, hkv, 16, d)),
+    kv = QuantKV(_arg(k_pool, "k_pool", codes), _arg(v_pool, "v_pool", codes, (n, hkv, 16, d)),
                  _arg(k_scale, "k_scale", _F32, (n, hkv)), _arg(v_scale, "v_scale", _F32, (n, hkv)),
                  _arg(k_tail, "k_tail", _BF16, tail), _arg(v_tail, "v_tail", _BF16, tail),
                  _arg(page_table, "page_table", _I32), None if err is None else _arg(err, "err", _I32, (1,)), fmt)
     kv.dims = (b, hkv, d, max_pages, n)
+    kv.device = k_pool.get_device()
     return kv
 
 
@@ -245,15 +258,24 @@ def make_block_index(bounds, scale, page_table, err=None) -> BlockIndex:
     ix = BlockIndex(_arg(bounds, "bounds", (torch.int8,)), _arg(scale, "scale", _F32, (n, hkv)),
                     _arg(page_table, "page_table", _I32), None if err is None else _arg(err, "err", _I32, (1,)))
     ix.dims = (b, hkv, d, max_pages, n)
+    ix.device = bounds.get_device()
     return ix
 
 
-def _dims(shape, *parts):
-    """The layer's sizes are those its 8-bit cache and block index were made with."""
+def _dims(shape, *parts, dev=None):
+    """The layer's sizes are those its caches and block index were made with (a bf16 cache may have more
+    sequences and pages), on the device of the call."""
     want = (shape.B, shape.Hkv, shape.D, shape.max_pages, shape.num_pages)
     for x in parts:
-        if x is not None and getattr(x, "dims", want) != want:
-            raise ValueError(f"{type(x).__name__} has (B, Hkv, D, max_pages, num_pages) {x.dims}, the shape {want}")
+        if x is None:
+            continue
+        have = getattr(x, "dims", want)
+        if have != want and not (type(x) is PagedKV and have and have[1:4] == want[1:4] and have[0] >= want[0]
+                                 and have[4] >= want[4]):
+            raise ValueError(f"{type(x).__name__} has (B, Hkv, D, max_pages, num_pages) "
+                             f"{have or 'of no pools of contiguous bf16 pages'}, the shape {want}")
+        if dev is not None and getattr(x, "device", dev) != dev:
+            raise ValueError(f"{type(x).__name__}: must be on the current CUDA device, is on device {x.device}")
 
 
 def _lens(B, lens, dev):
@@ -413,14 +435,14 @@ def sfi_selftest_wait(kv, limit_ns: int, stream=None):
 # ---------------------------------------------------------------- 8-bit cache, block-sparse attention
 def sfi_quant_store(shape, kv, qkv, pos_lo, L, lens=None, index=None, stream=None):
     dev = torch.cuda.current_device()
-    _dims(shape, qkv, index)
+    _dims(shape, kv, qkv, index, dev=dev)
     _check(lib().sfi_quant_store(C.byref(shape), C.byref(kv), C.byref(qkv), _ref(index), pos_lo, L,
                                  _lens(shape.B, lens, dev), _on(stream, dev)), "sfi_quant_store")
 
 
 def sfi_quant_append(shape, qkv, L, k_new, v_new, lens=None, index=None, stream=None):
     dev = torch.cuda.current_device()
-    _dims(shape, qkv, index)
+    _dims(shape, qkv, index, dev=dev)
     tok = (shape.B, shape.Hkv, shape.D)
     _check(lib().sfi_quant_append(C.byref(shape), C.byref(qkv), _ref(index), L, _lens(shape.B, lens, dev),
                                   _arg(k_new, "k_new", _BF16, tok, dev), _arg(v_new, "v_new", _BF16, tok, dev),
@@ -429,14 +451,14 @@ def sfi_quant_append(shape, qkv, L, k_new, v_new, lens=None, index=None, stream=
 
 def sfi_quant_load(shape, qkv, kv, pos_lo, L, lens=None, stream=None):
     dev = torch.cuda.current_device()
-    _dims(shape, qkv)
+    _dims(shape, qkv, kv, dev=dev)
     _check(lib().sfi_quant_load(C.byref(shape), C.byref(qkv), C.byref(kv), pos_lo, L, _lens(shape.B, lens, dev),
                                 _on(stream, dev)), "sfi_quant_load")
 
 
 def sfi_quant_attn(shape, qkv, L, q, out, ws, lens=None, lse=None, stream=None):
     dev = torch.cuda.current_device()
-    _dims(shape, qkv)
+    _dims(shape, qkv, dev=dev)
     q, out, lse = _attn_args(shape, q, out, lse, dev)
     _check(lib().sfi_quant_attn(C.byref(shape), C.byref(qkv), L, _lens(shape.B, lens, dev), q, out, lse,
                                 *_ws(ws, dev), _on(stream, dev)), "sfi_quant_attn")
@@ -450,7 +472,7 @@ def sfi_quant_poll_error(qkv) -> int:
 
 def sfi_block_build(shape, kv, index, pos_lo, L, lens=None, stream=None):
     dev = torch.cuda.current_device()
-    _dims(shape, index)
+    _dims(shape, kv, index, dev=dev)
     _check(lib().sfi_block_build(C.byref(shape), C.byref(kv), C.byref(index), pos_lo, L, _lens(shape.B, lens, dev),
                                  _on(stream, dev)), "sfi_block_build")
 
@@ -464,7 +486,7 @@ def sfi_block_workspace_size(shape: Shape) -> int:
 def sfi_block_select(shape, index, L, q, n_sink, n_recent, K, sel, ws, lens=None, stream=None):
     """sel: int32 [B, Hkv, at least K]."""
     dev = torch.cuda.current_device()
-    _dims(shape, index)
+    _dims(shape, index, dev=dev)
     _check(lib().sfi_block_select(C.byref(shape), C.byref(index), L, _lens(shape.B, lens, dev),
                                   _arg(q, "q", _BF16, (shape.B, shape.Hq, shape.D), dev), n_sink, n_recent, K,
                                   *_sel(shape, sel, dev), *_ws(ws, dev), _on(stream, dev)),
@@ -474,6 +496,7 @@ def sfi_block_select(shape, index, L, q, n_sink, n_recent, K, sel, ws, lens=None
 def sfi_block_attn(shape, kv, L, q, sel, K, out, ws, lens=None, lse=None, stream=None):
     """Attention over blocks sel[:, :, :K] of the bf16 cache."""
     dev = torch.cuda.current_device()
+    _dims(shape, kv, dev=dev)
     q, out, lse = _attn_args(shape, q, out, lse, dev)
     _check(lib().sfi_block_attn(C.byref(shape), C.byref(kv), L, _lens(shape.B, lens, dev), q,
                                 *_sel(shape, sel, dev), K, out, lse, *_ws(ws, dev), _on(stream, dev)),
@@ -483,7 +506,7 @@ def sfi_block_attn(shape, kv, L, q, sel, K, out, ws, lens=None, lse=None, stream
 def sfi_quant_block_attn(shape, qkv, L, q, sel, K, out, ws, lens=None, lse=None, stream=None):
     """sfi_block_attn on the 8-bit cache."""
     dev = torch.cuda.current_device()
-    _dims(shape, qkv)
+    _dims(shape, qkv, dev=dev)
     q, out, lse = _attn_args(shape, q, out, lse, dev)
     _check(lib().sfi_quant_block_attn(C.byref(shape), C.byref(qkv), L, _lens(shape.B, lens, dev), q,
                                       *_sel(shape, sel, dev), K, out, lse, *_ws(ws, dev),
