@@ -1,4 +1,5 @@
-"""Block selection over rows longer than one CTA's shared memory."""
+"""Block selection over rows longer than one CTA's shared memory; ranges, bad pages and bad
+lengths of the cache calls."""
 import numpy as np
 import pytest
 import torch
@@ -6,7 +7,7 @@ import torch
 from oracle import pages_oracle as P
 from slow_sparse_kv_sfi_b200 import sfi as S
 
-from test_gpu_pages import DEV, PAGE
+from test_gpu_pages import DEV, FMTS, PAGE, Case
 
 pytestmark = pytest.mark.gpu
 
@@ -67,3 +68,92 @@ def test_select_long_rows(D, Hq, Hkv, blocks, K, what):
             assert np.array_equal(got[b, h, :K], P.select(u, lens[b], n_sink, n_recent, K)), (b, h)
     assert int(err.item()) == ((5 | (14 << 8)) if reached else 0)
     assert reached == (what == "bad pages")
+
+
+# ------------------------------------------------------------------ ranges of sfi_quant_load, bad pages
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("D,Hkv", [(64, 3), (128, 2)])
+@pytest.mark.parametrize("lo", [16, 32, 64])
+def test_load_from_a_later_page(fmt, D, Hkv, lo):
+    """[pos_lo, len) of every sequence, whether it ends before pos_lo, there, inside its page or later;
+    every other row is left alone."""
+    lens = [100, lo - 5, lo, lo + 7, 0, 96, lo + 16]
+    c = Case(len(lens), Hkv, Hkv, D, lens, fmt, seed=42, slack=1).up()
+    S.sfi_quant_store(c.shape, c.kv, c.q8, 0, c.L, lens=c.lend)
+    k2, v2 = torch.full_like(c.kd, 9.0), torch.full_like(c.vd, 9.0)
+    S.sfi_quant_load(c.shape, c.q8, S.make_kv(k2, v2, c.ptd, None, c.err), lo, c.L, lens=c.lend)
+    assert c.error() == 0
+    want_k, want_v = torch.full_like(c.k, 9.0), torch.full_like(c.v, 9.0)
+    for b, n in enumerate(lens):
+        for want, which in ((want_k, "k"), (want_v, "v")):
+            for h in range(Hkv):
+                rows = torch.from_numpy(c.quant_rows(which, b, h, n)).float().to(torch.bfloat16)
+                for t in range(lo, n):
+                    want[int(c.pt[b, t // PAGE]), h, t % PAGE] = rows[t]
+    assert torch.equal(k2.cpu(), want_k) and torch.equal(v2.cpu(), want_v)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_load_with_bad_pages_and_lengths(fmt):
+    """A page number outside the pool, in either table, and a length outside [0, L]: latched, and what
+    they name is passed over."""
+    lens = [60, 48]
+    c = Case(2, 2, 2, 64, lens, fmt, seed=43, slack=1).up()
+    S.sfi_quant_store(c.shape, c.kv, c.q8, 0, c.L, lens=c.lend)
+    good_k, good_v = torch.full_like(c.kd, 9.0), torch.full_like(c.vd, 9.0)
+    S.sfi_quant_load(c.shape, c.q8, S.make_kv(good_k, good_v, c.ptd, None, c.err), 0, c.L, lens=c.lend)
+    assert c.error() == 0
+    err2 = torch.zeros(1, dtype=torch.int32, device=DEV)
+    for bad in (-1, c.n, 2 ** 31 - 1):
+        other = c.ptd.clone()
+        other[0, 1] = bad
+        want_k, want_v = good_k.clone(), good_v.clone()
+        want_k[int(c.pt[0, 1])] = 9.0
+        want_v[int(c.pt[0, 1])] = 9.0
+        for where in ("target", "source"):
+            k2, v2 = torch.full_like(c.kd, 9.0), torch.full_like(c.vd, 9.0)
+            kv2 = S.make_kv(k2, v2, other if where == "target" else c.ptd, None, err2)
+            q2 = S.make_quant_kv(c.kc, c.vc, c.ks, c.vs, c.ktail, c.vtail, other if where == "source" else c.ptd,
+                                 c.q8.format, c.err)
+            S.sfi_quant_load(c.shape, q2, kv2, 0, c.L, lens=c.lend)
+            assert S.sfi_quant_poll_error(q2) == (5 | (13 << 8) if where == "source" else 0)
+            assert S.sfi_poll_error(kv2) == (5 | (13 << 8) if where == "target" else 0)
+            assert torch.equal(k2, want_k) and torch.equal(v2, want_v)
+    for bad in (-3, c.L + 1, 2 ** 31 - 1):
+        k2, v2 = torch.full_like(c.kd, 9.0), torch.full_like(c.vd, 9.0)
+        ln = torch.tensor([bad, 48], dtype=torch.int32, device=DEV)
+        S.sfi_quant_load(c.shape, c.q8, S.make_kv(k2, v2, c.ptd, None, err2), 0, c.L, lens=ln)
+        assert S.sfi_quant_poll_error(c.q8) == 5 | (12 << 8)
+        want_k = torch.full_like(c.kd, 9.0)
+        for j in range(3):
+            want_k[int(c.pt[1, j])] = good_k[int(c.pt[1, j])]
+        assert torch.equal(k2, want_k)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_append_that_fills_a_page_nobody_has(fmt):
+    """The page number is looked up when the page fills: a bad one is latched, the token still reaches
+    the tail, and no page is written; the other sequence's page and a sound index are."""
+    c = Case(2, 4, 2, 128, [32, 32], fmt, seed=44).up()
+    S.sfi_quant_store(c.shape, c.kv, c.q8, 0, 31, index=c.ix)
+    tok_k = torch.stack([c.kd[int(c.pt[b, 1]), :, 15] for b in range(2)]).contiguous()
+    tok_v = torch.stack([c.vd[int(c.pt[b, 1]), :, 15] for b in range(2)]).contiguous()
+    before = c.kc.clone(), c.vc.clone(), c.ks.clone(), c.bounds.clone()
+    for bad in (-1, c.n, 2 ** 31 - 1):
+        other = c.ptd.clone()
+        other[0, 1] = bad
+        for table, index_table in ((other, c.ptd), (c.ptd, other)):
+            c.kc.copy_(before[0]), c.vc.copy_(before[1]), c.ks.copy_(before[2]), c.bounds.copy_(before[3])
+            ix_err = torch.zeros(1, dtype=torch.int32, device=DEV)
+            q2 = S.make_quant_kv(c.kc, c.vc, c.ks, c.vs, c.ktail, c.vtail, table, c.q8.format, c.err)
+            ix = S.make_block_index(c.bounds, c.bscale, index_table, ix_err)
+            S.sfi_quant_append(c.shape, q2, 32, tok_k, tok_v, index=ix)
+            code = 5 | (13 << 8)
+            assert S.sfi_quant_poll_error(q2) == (code if table is other else 0)
+            assert int(ix_err.item()) == (code if index_table is other else 0)
+            p0, p1 = int(c.pt[0, 1]), int(c.pt[1, 1])
+            assert torch.equal(c.ktail[:, :, 15], tok_k) and torch.equal(c.vtail[:, :, 15], tok_v)
+            changed = (c.kc != before[0]).flatten(1).any(1)
+            assert bool(changed[p1]) and bool(changed[p0]) == (table is not other) and int(changed.sum()) == 1 + (table is not other)
+            seen = (c.bounds != before[3]).flatten(1).any(1)
+            assert bool(seen[p1]) and bool(seen[p0]) == (index_table is not other) and int(seen.sum()) == 1 + (index_table is not other)
