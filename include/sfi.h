@@ -444,7 +444,10 @@ sfi_status sfi_quant_load(const sfi_shape* shape, const sfi_quant_kv* qkv, const
  * one.  An empty sequence gets out = 0 and lse = -infinity.  ws: scratch of
  * sfi_block_workspace_size bytes, 16-byte aligned, zero-filled before its first
  * use; every call leaves it ready for the next one that takes it, of any shape
- * whose size it has.  Calls that share one ws must not run concurrently. */
+ * whose size it has.  Calls that share one ws must not run concurrently: the
+ * counts in it tell which CTA has a row's last piece.  A count that no call can
+ * have left (a ws that was never zero) is latched as SFI_ERR_DEVICE_CHECK: that
+ * call's output does not stand, and the ws has to be zero-filled. */
 sfi_status sfi_quant_attn(const sfi_shape* shape, const sfi_quant_kv* qkv, int32_t L, const int32_t* lens,
                           const sfi_bf16* q, float* out, float* lse, void* ws, size_t ws_bytes,
                           sfi_stream stream);

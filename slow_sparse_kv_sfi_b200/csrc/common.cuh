@@ -48,6 +48,7 @@ enum ErrSite : int {
   kSiteAttnPage = 5, kSiteAttnRows = 6, kSiteCompactIdx = 7, kSiteCompactPage = 8,
   kSiteSelectPage = 9, kSiteCompactRows = 10, kSiteSelfTest = 11,
   kSiteLens = 12, kSiteQuantPage = 13, kSiteBlockPage = 14, kSitePageAttn = 15,
+  kSiteArrived = 16,
 };
 
 __device__ __forceinline__ void latch_error(int* err, int status, int site) {

@@ -856,10 +856,12 @@ __device__ __forceinline__ void attend_row(const PageAttnArgs& a, uint8_t* smem,
   int* last = reinterpret_cast<int*>(sml);   // the warps' (m, l) are used up
   if (threadIdx.x == 0) {
     // releases the CTA's piece (written before the barrier), acquires the others'
-    int before;
-    asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(before) : "l"(a.arrived + bh) : "memory");
-    const bool all = before == c1 - c0;
+    uint32_t before;
+    asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(before) : "l"(a.arrived + bh) : "memory");
+    const bool all = before == (uint32_t)(c1 - c0);
     if (all) a.arrived[bh] = 0;   // for the next call
+    // more than the row has pieces: the workspace was not zero
+    if (before > (uint32_t)(c1 - c0)) latch_error(a.err, SFI_ERR_DEVICE_CHECK, kSiteArrived);
     *last = all;
   }
   __syncthreads();

@@ -1,5 +1,5 @@
 """Block selection over rows longer than one CTA's shared memory; ranges, bad pages and bad
-lengths of the cache calls."""
+lengths of the cache calls; a workspace that was not zero."""
 import numpy as np
 import pytest
 import torch
@@ -157,3 +157,22 @@ def test_append_that_fills_a_page_nobody_has(fmt):
             assert bool(changed[p1]) and bool(changed[p0]) == (table is not other) and int(changed.sum()) == 1 + (table is not other)
             seen = (c.bounds != before[3]).flatten(1).any(1)
             assert bool(seen[p1]) and bool(seen[p0]) == (index_table is not other) and int(seen.sum()) == 1 + (index_table is not other)
+
+
+@pytest.mark.parametrize("fill", [0x7F, 0xFF, 0x01])
+def test_workspace_that_was_not_zero_is_latched(fill):
+    """Counts that no call can have left: latched, whatever the number of a row's pieces; after a zero fill
+    the call gives its result again."""
+    c = Case(2, 8, 2, 64, [4000, 1500], "int8", seed=45).up()
+    S.sfi_quant_store(c.shape, c.kv, c.q8, 0, c.L, lens=c.lend)
+    S.sfi_quant_attn(c.shape, c.q8, c.L, c.qd, c.out, c.ws, lens=c.lend)
+    assert c.error() == 0
+    want = c.out.clone()
+    c.ws.fill_(fill)
+    S.sfi_quant_attn(c.shape, c.q8, c.L, c.qd, c.out, c.ws, lens=c.lend)
+    assert c.error() == 5 | (16 << 8)
+    c.ws.zero_()
+    c.out.fill_(float("nan"))
+    S.sfi_quant_attn(c.shape, c.q8, c.L, c.qd, c.out, c.ws, lens=c.lend)
+    assert c.error() == 0
+    assert torch.equal(c.out, want)
