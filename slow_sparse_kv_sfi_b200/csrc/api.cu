@@ -138,12 +138,6 @@ sfi_status check_packed(const sfi_shape* s, const sfi_params* p, const sfi_packe
   return SFI_OK;
 }
 
-#define SFI_TRY(x)                     \
-  do {                                 \
-    sfi_status _r = (x);               \
-    if (_r != SFI_OK) return _r;       \
-  } while (0)
-
 }  // namespace
 
 // Arguments of a dense-attention call (all but the scratch): shared by the

@@ -58,11 +58,6 @@ __device__ __forceinline__ void mma_s8_16832(int (&d)[4], const uint32_t (&a)[4]
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ float tame(float x) {
-  const float big = __uint_as_float(0x7f7f0000u);
-  return x != x ? 0.f : fminf(fmaxf(x, -big), big);
-}
-
 constexpr float kScoreUnit = 1.f / 65536.f;
 
 // The score from x = 2^-16 max_h sum * e_h and the page's scale: below 1 the
@@ -514,12 +509,6 @@ cudaError_t launch_select(const SelectArgs& a, int BH, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, k, a);
 }
 
-#define SFI_TRY(x)               \
-  do {                           \
-    sfi_status _r = (x);         \
-    if (_r != SFI_OK) return _r; \
-  } while (0)
-
 }  // namespace
 
 // The arrival counts come first and have one size: a workspace may then serve
@@ -606,11 +595,7 @@ sfi_status sfi_block_select(const sfi_shape* shape, const sfi_block_index* index
                              : (wide ? block_score_kernel<64, 2> : block_score_kernel<64, 1>);
     e = launch_k(k, dim3(gx, BH), dim3(kThreads), 0, st, a);
   }
-  if (e != cudaSuccess) {
-    cudaGetLastError();
-    return SFI_ERR_CUDA;
-  }
-  if (nb <= kMaxRow) return SFI_OK;
+  if (e != cudaSuccess || nb <= kMaxRow) return cuda_status(e);
   return run_topk(BH, nb, a.scores, a.ld, K, 0, sel, sel_ld, nullptr, 0, st);
 }
 

@@ -238,6 +238,12 @@ __device__ __forceinline__ uint32_t float_key(float f) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
+// NaN -> 0, +-infinity -> +-largest finite bf16.
+__device__ __forceinline__ float tame(float x) {
+  const float big = __uint_as_float(0x7f7f0000u);
+  return x != x ? 0.f : fminf(fmaxf(x, -big), big);
+}
+
 // The smallest e >= -126 with amax <= 127 * 2^e (amax finite, >= 0): the
 // exponent field gives 2^x <= amax < 2^(x+1), and amax / 2^x is at most
 // 127 / 64 = 1.984375 unless its mantissa field exceeds 0x7e0000.

@@ -134,12 +134,6 @@ CtxLayout ctx_layout(const sfi_shape& s, const sfi_params& p, int n_layers) {
   return c;
 }
 
-#define SFI_TRY(x)               \
-  do {                           \
-    sfi_status _r = (x);         \
-    if (_r != SFI_OK) return _r; \
-  } while (0)
-
 sfi_status cu(cudaError_t e) { return e == cudaSuccess ? SFI_OK : SFI_ERR_CUDA; }
 
 // Event pair for one timed launch, or nulls when timing is off.

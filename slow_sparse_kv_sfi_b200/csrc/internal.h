@@ -117,6 +117,20 @@ struct StepToken {
   const sfi_bf16* v_new;
 };
 
+// Leaves the calling entry point with the status of x unless it is SFI_OK.
+#define SFI_TRY(x)               \
+  do {                           \
+    sfi_status _r = (x);         \
+    if (_r != SFI_OK) return _r; \
+  } while (0)
+
+// The status of a launch; a failed one does not stay the thread's last error.
+inline sfi_status cuda_status(cudaError_t e) {
+  if (e == cudaSuccess) return SFI_OK;
+  cudaGetLastError();
+  return SFI_ERR_CUDA;
+}
+
 // Argument checks shared by the entry points (api.cu): sizes of a layer, a
 // bf16 paged cache, a context length, and pointers copied 16 bytes at a time.
 sfi_status check_shape(const sfi_shape* s);
@@ -197,7 +211,6 @@ sfi_status run_idx_to_bits(const sfi_shape& s, const sfi_params& p, const sfi_pa
 int compact_tiles(int nC);
 int score_tile(int G);
 int stat_chunks(int nC);
-
 
 // Block-sparse and 8-bit calls: scratch is [arrival counts, zero between
 // calls][scores][partials (O)][partials (m, l)].

@@ -750,37 +750,37 @@ __device__ __forceinline__ void attend_row(const PageAttnArgs& a, uint8_t* smem,
       float zt[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) zt[nt][0] = zt[nt][1] = a.scale_log2;
-        tile_math<D, HM, false, true, kUnroll>(
-            st, zt, a.tail_unit, kBias, tail_rows, lane,
-            [&](int k, uint32_t (&f)[4]) {
-              const int d = C::k_col(t, k);
-              uint2 x = make_uint2(0, 0), y = make_uint2(0, 0);
-              if (g < tail_rows) x = __ldg(reinterpret_cast<const uint2*>(kt + g * D + d));
-              if (g + 8 < tail_rows) y = __ldg(reinterpret_cast<const uint2*>(kt + (g + 8) * D + d));
-              f[0] = x.x;
-              f[1] = y.x;
-              f[2] = x.y;
-              f[3] = y.y;
-            },
-            [&](int nt, int k, uint32_t& b0, uint32_t& b1) {
-              const uint2 x = q_at(nt, k);
-              b0 = x.x;
-              b1 = x.y;
-            },
-            []() {},
-            [&](int k, uint32_t (&f)[4]) {
-              const int d = C::v_col(g, k);
-              uint32_t x[4];
+      tile_math<D, HM, false, true, kUnroll>(
+          st, zt, a.tail_unit, kBias, tail_rows, lane,
+          [&](int k, uint32_t (&f)[4]) {
+            const int d = C::k_col(t, k);
+            uint2 x = make_uint2(0, 0), y = make_uint2(0, 0);
+            if (g < tail_rows) x = __ldg(reinterpret_cast<const uint2*>(kt + g * D + d));
+            if (g + 8 < tail_rows) y = __ldg(reinterpret_cast<const uint2*>(kt + (g + 8) * D + d));
+            f[0] = x.x;
+            f[1] = y.x;
+            f[2] = x.y;
+            f[3] = y.y;
+          },
+          [&](int nt, int k, uint32_t& b0, uint32_t& b1) {
+            const uint2 x = q_at(nt, k);
+            b0 = x.x;
+            b1 = x.y;
+          },
+          []() {},
+          [&](int k, uint32_t (&f)[4]) {
+            const int d = C::v_col(g, k);
+            uint32_t x[4];
 #pragma unroll
-              for (int r = 0; r < 4; ++r) {
-                const int tok = 2 * t + (r & 1) + 8 * (r >> 1);
-                x[r] = tok < tail_rows ? __ldg(reinterpret_cast<const uint32_t*>(vt + tok * D + d)) : 0u;
-              }
-              f[0] = __byte_perm(x[0], x[1], 0x5410);
-              f[1] = __byte_perm(x[0], x[1], 0x7632);
-              f[2] = __byte_perm(x[2], x[3], 0x5410);
-              f[3] = __byte_perm(x[2], x[3], 0x7632);
-            });
+            for (int r = 0; r < 4; ++r) {
+              const int tok = 2 * t + (r & 1) + 8 * (r >> 1);
+              x[r] = tok < tail_rows ? __ldg(reinterpret_cast<const uint32_t*>(vt + tok * D + d)) : 0u;
+            }
+            f[0] = __byte_perm(x[0], x[1], 0x5410);
+            f[1] = __byte_perm(x[0], x[1], 0x7632);
+            f[2] = __byte_perm(x[2], x[3], 0x5410);
+            f[3] = __byte_perm(x[2], x[3], 0x7632);
+          });
     }
     if (nxt.page >= 0) load_v(nxt);
     cur = nxt;
@@ -1064,18 +1064,6 @@ __global__ void __launch_bounds__(kMergeThreads) page_merge_kernel(const __grid_
   o = make_float4(o.x * r, o.y * r, o.z * r, o.w * r);
   l *= __uint_as_float((uint32_t)(127 + k) << 23);
   write_out<D>(a, (size_t)b * a.Hq + hq, slot * 4, M, l, o);
-}
-
-#define SFI_TRY(x)               \
-  do {                           \
-    sfi_status _r = (x);         \
-    if (_r != SFI_OK) return _r; \
-  } while (0)
-
-sfi_status cuda_status(cudaError_t e) {
-  if (e == cudaSuccess) return SFI_OK;
-  cudaGetLastError();
-  return SFI_ERR_CUDA;
 }
 
 // Rows of one length get the same number of CTAs each where that makes no run

@@ -66,12 +66,6 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
-// NaN -> 0, +-infinity -> +-largest finite bf16.
-__device__ __forceinline__ float tame(float x) {
-  const float big = __uint_as_float(0x7f7f0000u);
-  return x != x ? 0.f : fminf(fmaxf(x, -big), big);
-}
-
 __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {   // bf16 pairs; NaN stays
   const __nv_bfloat162 r = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
   return *reinterpret_cast<const uint32_t*>(&r);
@@ -440,18 +434,6 @@ sfi_status check_range(const sfi_shape* s, int pos_lo, int L) {
   return SFI_OK;
 }
 
-sfi_status launched(cudaError_t e) {
-  if (e == cudaSuccess) return SFI_OK;
-  cudaGetLastError();
-  return SFI_ERR_CUDA;
-}
-
-#define SFI_TRY(x)               \
-  do {                           \
-    sfi_status _r = (x);         \
-    if (_r != SFI_OK) return _r; \
-  } while (0)
-
 }  // namespace
 
 sfi_status check_quant(const sfi_quant_kv* q) {
@@ -495,7 +477,7 @@ sfi_status sfi_quant_store(const sfi_shape* shape, const sfi_paged_kv* kv, const
   const bool e4 = qkv->format == SFI_FMT_E4M3;
   auto k = shape->D == 128 ? (e4 ? store_kernel<128, SFI_FMT_E4M3> : store_kernel<128, SFI_FMT_INT8>)
                            : (e4 ? store_kernel<64, SFI_FMT_E4M3> : store_kernel<64, SFI_FMT_INT8>);
-  return launched(launch_k(k, dim3((unsigned)((units + kRangeWarps - 1) / kRangeWarps), shape->B), dim3(kRangeWarps * 32), 0, (cudaStream_t)stream, a,
+  return cuda_status(launch_k(k, dim3((unsigned)((units + kRangeWarps - 1) / kRangeWarps), shape->B), dim3(kRangeWarps * 32), 0, (cudaStream_t)stream, a,
                            (int)units));
 }
 
@@ -517,7 +499,7 @@ sfi_status sfi_quant_append(const sfi_shape* shape, const sfi_quant_kv* qkv, con
   const bool e4 = qkv->format == SFI_FMT_E4M3;
   auto k = shape->D == 128 ? (e4 ? append_quant_kernel<128, SFI_FMT_E4M3> : append_quant_kernel<128, SFI_FMT_INT8>)
                            : (e4 ? append_quant_kernel<64, SFI_FMT_E4M3> : append_quant_kernel<64, SFI_FMT_INT8>);
-  return launched(
+  return cuda_status(
       launch_k(k, dim3((unsigned)((units + 3) / 4)), dim3(128), 0, (cudaStream_t)stream, a, (int)units));
 }
 
@@ -537,7 +519,7 @@ sfi_status sfi_quant_load(const sfi_shape* shape, const sfi_quant_kv* qkv, const
   const bool e4 = qkv->format == SFI_FMT_E4M3;
   auto k = shape->D == 128 ? (e4 ? load_kernel<128, SFI_FMT_E4M3> : load_kernel<128, SFI_FMT_INT8>)
                            : (e4 ? load_kernel<64, SFI_FMT_E4M3> : load_kernel<64, SFI_FMT_INT8>);
-  return launched(launch_k(k, dim3((unsigned)((units + kRangeWarps - 1) / kRangeWarps), shape->B), dim3(kRangeWarps * 32), 0, (cudaStream_t)stream, a,
+  return cuda_status(launch_k(k, dim3((unsigned)((units + kRangeWarps - 1) / kRangeWarps), shape->B), dim3(kRangeWarps * 32), 0, (cudaStream_t)stream, a,
                            (int)units));
 }
 
@@ -556,7 +538,7 @@ sfi_status sfi_block_build(const sfi_shape* shape, const sfi_paged_kv* kv, const
   const long units = (long)n_pages * shape->Hkv;
   if (units > 0x7fffff00L || shape->B > 65535) return SFI_ERR_UNSUPPORTED;
   auto k = shape->D == 128 ? store_kernel<128, kNoFormat> : store_kernel<64, kNoFormat>;
-  return launched(launch_k(k, dim3((unsigned)((units + kRangeWarps - 1) / kRangeWarps), shape->B), dim3(kRangeWarps * 32), 0, (cudaStream_t)stream, a,
+  return cuda_status(launch_k(k, dim3((unsigned)((units + kRangeWarps - 1) / kRangeWarps), shape->B), dim3(kRangeWarps * 32), 0, (cudaStream_t)stream, a,
                            (int)units));
 }
 
