@@ -176,3 +176,88 @@ def test_workspace_that_was_not_zero_is_latched(fill):
     S.sfi_quant_attn(c.shape, c.q8, c.L, c.qd, c.out, c.ws, lens=c.lend)
     assert c.error() == 0
     assert torch.equal(c.out, want)
+
+
+@pytest.mark.parametrize("D,Hq,Hkv,nb,K", [(64, 2, 1, 262144, 1000), (64, 80, 80, 33000, 30), (128, 40, 40, 131073, 50)])
+def test_select_longest_and_many_long_rows(D, Hq, Hkv, nb, K):
+    """The most blocks there may be, and so many long rows that they do not all run at once."""
+    g = torch.Generator().manual_seed(46)
+    pool = 300
+    bounds = torch.randint(-127, 128, (pool, Hkv, 2, D), generator=g).to(torch.int8)
+    bounds = torch.stack([bounds.amax(2), bounds.amin(2)], dim=2)
+    scale = torch.exp2(torch.randint(-3, 3, (pool, Hkv), generator=g).float())
+    pt = torch.randint(0, pool, (1, nb), generator=g, dtype=torch.int32)
+    q = (torch.randn(1, Hq, D, generator=g) * 3).to(torch.bfloat16)
+    shape = S.make_shape(1, Hq, Hkv, D, nb, pool)
+    d = [t.to(DEV).contiguous() for t in (bounds, scale, pt)]
+    ix = S.make_block_index(*d)
+    ws = torch.zeros(S.sfi_block_workspace_size(shape), dtype=torch.uint8, device=DEV)
+    sel = torch.empty(1, Hkv, K, dtype=torch.int32, device=DEV)
+    n = nb * PAGE - 1
+    S.sfi_block_select(shape, ix, n, q.to(DEV), 4, 64, K, sel, ws)
+    torch.cuda.synchronize()
+    G = Hq // Hkv
+    for h in range(Hkv):
+        u = P.block_scores(q[0, h * G:(h + 1) * G].double().numpy(), bounds[:, h].numpy().astype(np.int64),
+                           scale[:, h].double().numpy())[pt[0].numpy()]
+        assert np.array_equal(sel[0, h].cpu().numpy(), P.select(u, n, 4, 64, K)), h
+    if nb == 262144:
+        one = S.make_shape(1, Hq, Hkv, D, nb + 1, pool)
+        ws = torch.zeros(S.sfi_block_workspace_size(one), dtype=torch.uint8, device=DEV)
+        more = S.make_block_index(d[0], d[1], torch.zeros(1, nb + 1, dtype=torch.int32, device=DEV))
+        with pytest.raises(S.SFIError):
+            S.sfi_block_select(one, more, nb * PAGE + 1, q.to(DEV), 4, 64, K, sel, ws)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("D,Hq", [(64, 2), (128, 16)])
+@pytest.mark.parametrize("ragged", [False, True])
+def test_attention_over_four_million_tokens(fmt, D, Hq, ragged):
+    """A row of 262145 pages (a few different ones, many times each) beside a short one: the definition with
+    every page counted as often as it occurs.  Sums of n tokens lose at most (tiles of a warp + pieces + 64)
+    steps of 2^-23: 262145 tiles over 148 or more CTAs of 4 or more warps, 443 a warp at most, and as many
+    pieces."""
+    nb, pool = 262145, 40
+    n = nb * PAGE - 11                       # the last page is not full
+    lens = [n, 20] if ragged else [n]
+    B = len(lens)
+    c = Case(B, Hq, 1, D, [pool * PAGE] + [20] * (B - 1), fmt, seed=47, spare=0).up()
+    S.sfi_quant_store(c.shape, c.kv, c.q8, 0, c.L, lens=c.lend)
+    own = c.pt[0].long()
+    pick = torch.randint(0, pool, (nb,), generator=c.g)
+    pt = torch.zeros(B, nb, dtype=torch.int32)
+    pt[0] = own[pick].to(torch.int32)
+    if ragged:
+        pt[1, :2] = c.pt[1, :2]
+    ptd = pt.to(DEV)
+    shape = S.make_shape(B, Hq, 1, D, nb, c.n)
+    kt, vt = (torch.randn(B, 1, PAGE, D, generator=c.g).to(torch.bfloat16) for _ in range(2))
+    ktd, vtd = kt.to(DEV), vt.to(DEV)
+    if ragged:
+        ktd[1], vtd[1] = c.ktail[1], c.vtail[1]
+    q8 = S.make_quant_kv(c.kc, c.vc, c.ks, c.vs, ktd, vtd, ptd, c.q8.format, c.err)
+    ws = torch.zeros(S.sfi_block_workspace_size(shape), dtype=torch.uint8, device=DEV)
+    ln = torch.tensor(lens, dtype=torch.int32, device=DEV) if ragged else None
+    S.sfi_quant_attn(shape, q8, n, c.qd, c.out, ws, lens=ln, lse=c.lse)
+    assert c.error() == 0
+    K, V = c.quant_rows("k", 0, 0, pool * PAGE), c.quant_rows("v", 0, 0, pool * PAGE)
+    times = np.bincount(pick[:nb - 1].numpy(), minlength=pool).astype(np.float64).repeat(PAGE)
+    K = np.concatenate([K, kt[0, 0, :5].double().numpy()])
+    V = np.concatenate([V, vt[0, 0, :5].double().numpy()])
+    times = np.concatenate([times, np.ones(5)])
+    q = c.q[0].double().numpy()
+    z = q @ K.T / np.sqrt(D)
+    m = z.max(1, keepdims=True)
+    w = np.exp(z - m) * times
+    total = w.sum(1, keepdims=True)
+    o, pv = w @ V / total, w @ np.abs(V) / total
+    s = (np.abs(q) @ np.abs(K).T).max(1) / np.sqrt(D)
+    dz = (D / 16 + 2) * 2.0 ** -23 * s + 2.0 ** -22 * s
+    steps = (2 * 443 + 64) * 2.0 ** -23
+    tol = (2.0 ** -16 + 2 * dz + steps)[:, None] * pv + np.minimum(2.0 ** -27, w / times / total) @ (times[:, None] * np.abs(V))
+    assert np.all(np.abs(c.out[0].cpu().double().numpy() - o) <= tol)
+    lse = (m + np.log(total))[:, 0]
+    assert np.all(np.abs(c.lse[0].cpu().double().numpy() - lse) <= 2 * dz + steps + 2.0 ** -22 * np.abs(lse))
+    if ragged:
+        o, _, pv, s = P.attention(c.q[1].double().numpy(), c.quant_rows("k", 1, 0, 20), c.quant_rows("v", 1, 0, 20))
+        assert np.all(np.abs(c.out[1].cpu().double().numpy() - o) <= 1e-4 * pv)
