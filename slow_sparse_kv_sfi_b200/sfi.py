@@ -212,6 +212,8 @@ def _arg(t, name, dtypes, shape=None, dev=None):
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# (the public call first looks whether CUDA is up, which the tensors of a call already show)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _on(stream, dev):
@@ -264,35 +266,36 @@ def make_block_index(bounds, scale, page_table, err=None) -> BlockIndex:
 
 def _dims(shape, *parts, dev=None):
     """The layer's sizes are those its caches and block index were made with (a bf16 cache may have more
-    sequences and pages), on the device of the call."""
-    want = (shape.B, shape.Hkv, shape.D, shape.max_pages, shape.num_pages)
+    sequences and pages), on the device of the call.  Returns B, Hkv, D."""
+    B, Hkv, D = shape.B, shape.Hkv, shape.D
+    want = (B, Hkv, D, shape.max_pages, shape.num_pages)
     for x in parts:
         if x is None:
             continue
         have = getattr(x, "dims", want)
-        if have != want and not (type(x) is PagedKV and have and have[1:4] == want[1:4] and have[0] >= want[0]
+        if have != want and not (type(x) is PagedKV and have and have[1:4] == want[1:4] and have[0] >= B
                                  and have[4] >= want[4]):
             raise ValueError(f"{type(x).__name__} has (B, Hkv, D, max_pages, num_pages) "
                              f"{have or 'of no pools of contiguous bf16 pages'}, the shape {want}")
         if dev is not None and getattr(x, "device", dev) != dev:
             raise ValueError(f"{type(x).__name__}: must be on the current CUDA device, is on device {x.device}")
+    return B, Hkv, D
 
 
 def _lens(B, lens, dev):
     return None if lens is None else _arg(lens, "lens", _I32, (B,), dev)
 
 
-def _attn_args(shape, q, out, lse, dev):
-    b, hq = shape.B, shape.Hq
-    qs = (b, hq, shape.D)
+def _attn_args(B, Hq, D, q, out, lse, dev):
+    qs = (B, Hq, D)
     return (_arg(q, "q", _BF16, qs, dev), _arg(out, "out", _F32, qs, dev),
-            None if lse is None else _arg(lse, "lse", _F32, (b, hq), dev))
+            None if lse is None else _arg(lse, "lse", _F32, (B, Hq), dev))
 
 
-def _sel(shape, sel, dev):
+def _sel(B, Hkv, sel, dev):
     size = sel.shape
-    if len(size) != 3 or size[0] != shape.B or size[1] != shape.Hkv:
-        raise ValueError(f"sel: shape {tuple(size)}, expected ({shape.B}, {shape.Hkv}, at least K)")
+    if len(size) != 3 or size[0] != B or size[1] != Hkv:
+        raise ValueError(f"sel: shape {tuple(size)}, expected ({B}, {Hkv}, at least K)")
     return _arg(sel, "sel", _I32, None, dev), size[2]
 
 
@@ -434,33 +437,33 @@ def sfi_selftest_wait(kv, limit_ns: int, stream=None):
 
 # ---------------------------------------------------------------- 8-bit cache, block-sparse attention
 def sfi_quant_store(shape, kv, qkv, pos_lo, L, lens=None, index=None, stream=None):
-    dev = torch.cuda.current_device()
-    _dims(shape, kv, qkv, index, dev=dev)
+    dev = _current_device()
+    B, Hkv, D = _dims(shape, kv, qkv, index, dev=dev)
     _check(lib().sfi_quant_store(C.byref(shape), C.byref(kv), C.byref(qkv), _ref(index), pos_lo, L,
-                                 _lens(shape.B, lens, dev), _on(stream, dev)), "sfi_quant_store")
+                                 _lens(B, lens, dev), _on(stream, dev)), "sfi_quant_store")
 
 
 def sfi_quant_append(shape, qkv, L, k_new, v_new, lens=None, index=None, stream=None):
-    dev = torch.cuda.current_device()
-    _dims(shape, qkv, index, dev=dev)
-    tok = (shape.B, shape.Hkv, shape.D)
-    _check(lib().sfi_quant_append(C.byref(shape), C.byref(qkv), _ref(index), L, _lens(shape.B, lens, dev),
+    dev = _current_device()
+    B, Hkv, D = _dims(shape, qkv, index, dev=dev)
+    tok = (B, Hkv, D)
+    _check(lib().sfi_quant_append(C.byref(shape), C.byref(qkv), _ref(index), L, _lens(B, lens, dev),
                                   _arg(k_new, "k_new", _BF16, tok, dev), _arg(v_new, "v_new", _BF16, tok, dev),
                                   _on(stream, dev)), "sfi_quant_append")
 
 
 def sfi_quant_load(shape, qkv, kv, pos_lo, L, lens=None, stream=None):
-    dev = torch.cuda.current_device()
-    _dims(shape, qkv, kv, dev=dev)
-    _check(lib().sfi_quant_load(C.byref(shape), C.byref(qkv), C.byref(kv), pos_lo, L, _lens(shape.B, lens, dev),
+    dev = _current_device()
+    B, Hkv, D = _dims(shape, qkv, kv, dev=dev)
+    _check(lib().sfi_quant_load(C.byref(shape), C.byref(qkv), C.byref(kv), pos_lo, L, _lens(B, lens, dev),
                                 _on(stream, dev)), "sfi_quant_load")
 
 
 def sfi_quant_attn(shape, qkv, L, q, out, ws, lens=None, lse=None, stream=None):
-    dev = torch.cuda.current_device()
-    _dims(shape, qkv, dev=dev)
-    q, out, lse = _attn_args(shape, q, out, lse, dev)
-    _check(lib().sfi_quant_attn(C.byref(shape), C.byref(qkv), L, _lens(shape.B, lens, dev), q, out, lse,
+    dev = _current_device()
+    B, Hkv, D = _dims(shape, qkv, dev=dev)
+    q, out, lse = _attn_args(B, shape.Hq, D, q, out, lse, dev)
+    _check(lib().sfi_quant_attn(C.byref(shape), C.byref(qkv), L, _lens(B, lens, dev), q, out, lse,
                                 *_ws(ws, dev), _on(stream, dev)), "sfi_quant_attn")
 
 
@@ -471,9 +474,9 @@ def sfi_quant_poll_error(qkv) -> int:
 
 
 def sfi_block_build(shape, kv, index, pos_lo, L, lens=None, stream=None):
-    dev = torch.cuda.current_device()
-    _dims(shape, kv, index, dev=dev)
-    _check(lib().sfi_block_build(C.byref(shape), C.byref(kv), C.byref(index), pos_lo, L, _lens(shape.B, lens, dev),
+    dev = _current_device()
+    B, Hkv, D = _dims(shape, kv, index, dev=dev)
+    _check(lib().sfi_block_build(C.byref(shape), C.byref(kv), C.byref(index), pos_lo, L, _lens(B, lens, dev),
                                  _on(stream, dev)), "sfi_block_build")
 
 
@@ -485,31 +488,31 @@ def sfi_block_workspace_size(shape: Shape) -> int:
 
 def sfi_block_select(shape, index, L, q, n_sink, n_recent, K, sel, ws, lens=None, stream=None):
     """sel: int32 [B, Hkv, at least K]."""
-    dev = torch.cuda.current_device()
-    _dims(shape, index, dev=dev)
-    _check(lib().sfi_block_select(C.byref(shape), C.byref(index), L, _lens(shape.B, lens, dev),
-                                  _arg(q, "q", _BF16, (shape.B, shape.Hq, shape.D), dev), n_sink, n_recent, K,
-                                  *_sel(shape, sel, dev), *_ws(ws, dev), _on(stream, dev)),
+    dev = _current_device()
+    B, Hkv, D = _dims(shape, index, dev=dev)
+    _check(lib().sfi_block_select(C.byref(shape), C.byref(index), L, _lens(B, lens, dev),
+                                  _arg(q, "q", _BF16, (B, shape.Hq, D), dev), n_sink, n_recent, K,
+                                  *_sel(B, Hkv, sel, dev), *_ws(ws, dev), _on(stream, dev)),
            "sfi_block_select")
 
 
 def sfi_block_attn(shape, kv, L, q, sel, K, out, ws, lens=None, lse=None, stream=None):
     """Attention over blocks sel[:, :, :K] of the bf16 cache."""
-    dev = torch.cuda.current_device()
-    _dims(shape, kv, dev=dev)
-    q, out, lse = _attn_args(shape, q, out, lse, dev)
-    _check(lib().sfi_block_attn(C.byref(shape), C.byref(kv), L, _lens(shape.B, lens, dev), q,
-                                *_sel(shape, sel, dev), K, out, lse, *_ws(ws, dev), _on(stream, dev)),
+    dev = _current_device()
+    B, Hkv, D = _dims(shape, kv, dev=dev)
+    q, out, lse = _attn_args(B, shape.Hq, D, q, out, lse, dev)
+    _check(lib().sfi_block_attn(C.byref(shape), C.byref(kv), L, _lens(B, lens, dev), q,
+                                *_sel(B, Hkv, sel, dev), K, out, lse, *_ws(ws, dev), _on(stream, dev)),
            "sfi_block_attn")
 
 
 def sfi_quant_block_attn(shape, qkv, L, q, sel, K, out, ws, lens=None, lse=None, stream=None):
     """sfi_block_attn on the 8-bit cache."""
-    dev = torch.cuda.current_device()
-    _dims(shape, qkv, dev=dev)
-    q, out, lse = _attn_args(shape, q, out, lse, dev)
-    _check(lib().sfi_quant_block_attn(C.byref(shape), C.byref(qkv), L, _lens(shape.B, lens, dev), q,
-                                      *_sel(shape, sel, dev), K, out, lse, *_ws(ws, dev),
+    dev = _current_device()
+    B, Hkv, D = _dims(shape, qkv, dev=dev)
+    q, out, lse = _attn_args(B, shape.Hq, D, q, out, lse, dev)
+    _check(lib().sfi_quant_block_attn(C.byref(shape), C.byref(qkv), L, _lens(B, lens, dev), q,
+                                      *_sel(B, Hkv, sel, dev), K, out, lse, *_ws(ws, dev),
                                       _on(stream, dev)), "sfi_quant_block_attn")
 
 
