@@ -494,7 +494,8 @@ sfi_status sfi_block_select(const sfi_shape* shape, const sfi_block_index* index
 /* Decode attention over the listed blocks of a bf16 paged cache and of an 8-bit
  * cache: the tokens below len of blocks sel[b, g, 0 .. K).  Entries outside
  * [0, ceil(len / 16)) are passed over; a block listed twice counts twice.  No
- * token left: out = 0, lse = -infinity.  The other arguments are those of
+ * token left: out = 0, lse = -infinity.  A bf16 value that is not finite makes
+ * its column of the outputs infinite or NaN.  The other arguments are those of
  * sfi_quant_attn.  sel_ld >= K >= 1, K <= max_pages.  The bf16 pools must be
  * 32-byte aligned here. */
 sfi_status sfi_block_attn(const sfi_shape* shape, const sfi_paged_kv* kv, int32_t L, const int32_t* lens,

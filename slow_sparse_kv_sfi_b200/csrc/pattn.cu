@@ -17,13 +17,13 @@
 //
 // Bound by reading the cache at G <= 8 (at G = 16 by the latency of 414
 // instructions a tile with 12 warps an SM), so the layout serves the loads: two
-// sequences of 128K e4m3, 32/8 heads, 537 MB, take 89 us, 6.0 TB/s; 16 of 64K with
-// 64/4 heads, 1.07 GB, 240 us.  Each thread loads
-// exactly the bytes its own matrix fragments need, 32 or 16 at a time, straight
-// into registers: the next tile's K while the softmax and V^T P^T of this one
-// run, its V while the next S^T does.  No shared memory, no barrier and no wait
-// that another warp has to end.  That works because the order of a contraction
-// is free:
+// sequences of 128K e4m3, 32/8 heads, 537 MB, take 89 us, 6.0 TB/s, in a short
+// graph and 97 in calls that go on for half a second (at the power cap); 16 of 64K
+// with 64/4 heads, 1.07 GB, 237 and 261 us.  Each thread loads exactly the bytes
+// its own matrix fragments need, 32 or 16 at a time, straight into registers: the
+// next tile's K while the softmax and V^T P^T of this one run, its V while the
+// next S^T does.  No shared memory, no barrier and no wait that another warp has
+// to end.  That works because the order of a contraction is free:
 //   S^T[16 tok x 8 heads] = K[16 x D] . Q^T[D x 8]: thread (g, t) of the
 //     fragment layout (g = lane / 4, t = lane % 4) holds rows g, g + 8 and any
 //     D / 4 of the columns, as long as Q is laid out alike: a run of them, so

@@ -261,3 +261,39 @@ def test_attention_over_four_million_tokens(fmt, D, Hq, ragged):
     if ragged:
         o, _, pv, s = P.attention(c.q[1].double().numpy(), c.quant_rows("k", 1, 0, 20), c.quant_rows("v", 1, 0, 20))
         assert np.all(np.abs(c.out[1].cpu().double().numpy() - o) <= 1e-4 * pv)
+
+
+def test_two_streams_with_workspaces_of_their_own():
+    """append -> select -> attend on two streams at once, each with its own workspace: the results of each
+    alone."""
+    cs = [Case(2, 16, 4, 128, [3000, 900], "e4m3", seed=48).up(), Case(3, 8, 2, 64, [2000, 64, 5000], "int8", seed=49).up()]
+    K = 12
+    sels = [torch.zeros(c.B, c.Hkv, K, dtype=torch.int32, device=DEV) for c in cs]
+
+    def step(c, sel, stream=None):
+        S.sfi_quant_append(c.shape, c.q8, c.L, c.kd[:c.B, :, 0].contiguous(), c.vd[:c.B, :, 0].contiguous(), lens=c.lend,
+                           index=c.ix, stream=stream)
+        S.sfi_block_select(c.shape, c.ix, c.L, c.qd, 4, 20, K, sel, c.ws, lens=c.lend, stream=stream)
+        S.sfi_quant_block_attn(c.shape, c.q8, c.L, c.qd, sel, K, c.out, c.ws, lens=c.lend, lse=c.lse, stream=stream)
+        S.sfi_quant_attn(c.shape, c.q8, c.L, c.qd, c.full, c.ws, lens=c.lend, stream=stream)
+
+    want = []
+    for c, sel in zip(cs, sels):
+        c.full = torch.empty_like(c.out)
+        S.sfi_quant_store(c.shape, c.kv, c.q8, 0, c.L, lens=c.lend - 1, index=c.ix)
+        step(c, sel)
+        torch.cuda.synchronize()
+        want.append([x.clone() for x in (sel, c.out, c.lse, c.full)])
+        for x in (sel, c.out, c.lse, c.full):
+            x.fill_(-7)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(25):
+        for c, sel, st in zip(cs, sels, streams):
+            with torch.cuda.stream(st):
+                step(c, sel, st)
+    torch.cuda.synchronize()
+    for c, sel, w in zip(cs, sels, want):
+        assert c.error() == 0
+        for x, y in zip((sel, c.out, c.lse, c.full), w):
+            assert torch.equal(x, y)
